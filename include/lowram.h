@@ -84,6 +84,8 @@ typedef enum lr_dtype { LR_F32 = 0, LR_BF16 = 1 } lr_dtype;
 #define LR_DEVERR_PTR 16        /* a residual block pointer out of [0, k] or decreasing */
 #define LR_DEVERR_TIMEOUT 32    /* a kernel gave up waiting on its own pipeline (its output is invalid) */
 #define LR_DEVERR_LAUNCH 64     /* a kernel found its shared memory misaligned and did not run (output invalid) */
+#define LR_DEVERR_PAGE 128      /* a page id outside [0, n_pages): the page's tokens skipped */
+#define LR_DEVERR_LEN 256       /* a sequence length or a token range out of bounds: the sequence skipped or clipped */
 
 typedef struct lr_cache_shape {
   int32_t batch;      /* B >= 0 */
@@ -400,6 +402,135 @@ lr_status lr_decode_attn_noalloc(const lr_cache_shape* shape, int32_t layer, int
                                  const void* res_val, const int32_t* res_blk_ptr, int32_t k,
                                  const int32_t* block_list, int32_t n_sel, float scale, void* o,
                                  lr_stream_t stream);
+
+/*
+ * lr_decode_attn_lse -- lr_decode_attn that also returns the log-sum-exp of every query head,
+ *   lse[b, hq] = log sum_{t in S} exp(scale * q[b, hq] . k~_t)   (-inf for an empty S),
+ * which lr_decode_attn_kv8 takes to join more tokens to the same softmax.
+ * Output: lse [B, Hq] fp32. Everything else is as lr_decode_attn.
+ */
+lr_status lr_decode_attn_lse(const lr_cache_shape* shape, int32_t layer, int32_t n_q_heads,
+                             const void* q, const void* A, const void* Bt,
+                             const lr_predictor* predictor, const int32_t* res_idx,
+                             const void* res_val, const int32_t* res_blk_ptr, int32_t k,
+                             const int32_t* block_list, int32_t n_sel, float scale, void* o, float* lse,
+                             void* ws, size_t ws_bytes, lr_stream_t stream);
+
+/* ------------------------------------------------------------------ 8-bit paged cache */
+
+/*
+ * Keys and values of one layer in pages of 64 tokens (LR_BLOCK_TOKENS), 8 bits per number, for
+ * what the compressed cache does not hold: layers and short contexts that are not packed, and
+ * tokens generated since the packing, with a length of its own for every sequence.
+ *
+ *   k_codes, v_codes [n_pages, Hkv, 64, hd] uint8: e4m3 codes (4 exponent bits, bias 7, 3
+ *                    mantissa bits, largest value 448, 0x7f / 0xff = NaN). Page p starts at byte
+ *                    p * page_stride; page_stride 0 means dense (Hkv * 64 * hd), any other value
+ *                    is a multiple of 16 and at least that (one pool may hold several layers, or
+ *                    K and V side by side).
+ *   k_scale, v_scale [n_pages, Hkv] fp32, positive: the value of a number is code * scale. The
+ *                    scales that lr_kv8_append writes are powers of two.
+ *   page_table       [B, max_pages] int32: token t of sequence b is row t % 64 of page
+ *                    page_table[b, t / 64]. Entries behind a sequence's last token are not read.
+ *   lens             [B] int32: tokens of each sequence, 0 <= lens[b] <= 64 max_pages. Sequences may
+ *                    share pages that only lr_decode_attn_kv8 reads.
+ * What pages hold behind a sequence's last token is never used (it may be NaN codes).
+ * dtype is the type of q, k, v and o beside the cache. A scale covers one page of one KV head.
+ */
+typedef struct lr_kv8_pages {
+  int32_t batch;      /* B >= 0 */
+  int32_t n_kv_heads; /* Hkv >= 1 */
+  int32_t head_dim;   /* hd: multiple of 8, <= 256 */
+  int32_t n_pages;    /* pages in the pool, >= 1 */
+  int32_t max_pages;  /* page_table entries per sequence, >= 1, at most 2^25 - 1 */
+  lr_dtype dtype;
+  int64_t page_stride;
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  float* k_scale;
+  float* v_scale;
+  const int32_t* page_table;
+  const int32_t* lens;
+} lr_kv8_pages;
+
+/*
+ * Rotary position embedding of the first rot_dim dims of a head (a multiple of 16, <= hd): the
+ * pair j of a token at position pos turns by the angle pos * inv_freq[j],
+ *     (x0, x1) -> (x0 cos - x1 sin, x1 cos + x0 sin),
+ * where pair j is dims (j, rot_dim / 2 + j), or (2j, 2j + 1) with interleaved = 1.
+ * inv_freq [rot_dim / 2] fp32 in radians per token. The angle is reduced exactly: it is right to
+ * about 1e-6 radians at every position an int32 can hold.
+ */
+typedef struct lr_rope {
+  const float* inv_freq;
+  int32_t rot_dim;
+  int32_t interleaved;
+} lr_rope;
+
+/* Workspace bytes lr_kv8_append needs. */
+size_t lr_kv8_append_workspace_bytes(const lr_kv8_pages* kv);
+
+/*
+ * lr_kv8_append -- new keys and values go into their pages, keys (and queries) rotated on the way.
+ *
+ * lens[b] counts the new tokens: with n_b new tokens of sequence b, token i gets position
+ * lens[b] - n_b + i, which is also its place in the cache. Per page and KV head that receives
+ * tokens, with a = the largest finite magnitude among this call's rows of it:
+ *   fresh = the smallest power of two with a <= 448 fresh, at least 2^-24;
+ *   scale = max(scale, fresh) where the page already holds tokens of the sequence: if that is
+ *           larger than the old scale, their codes become round(code * old / scale);
+ *   scale = fresh where it does not (what the page and its scale held before is not read);
+ *   code  = round(x / scale), to nearest even; NaN and infinities become NaN codes and do not
+ *           count towards a.
+ * Keys are rotated in fp32 and rounded once, to the code. Rows behind the new tokens and every
+ * other page keep their bytes. The result does not depend on the order of execution; calls with
+ * the same new tokens in the same places may be repeated.
+ *
+ * Inputs:  k, v [n_tokens, Hkv, hd] and q [n_tokens, Hq, hd] in kv->dtype, the sequences' new
+ *          tokens one after another; k_stride, v_stride, q_stride: elements from one token to the
+ *          next (0 = dense), whole 16 bytes, so that the three may be views of one fused tensor.
+ *          cu_tokens [B + 1] ascending: sequence b has rows cu_tokens[b] .. cu_tokens[b + 1] (none
+ *          is allowed); NULL: one token for each sequence, n_tokens = B, and a sequence with
+ *          lens[b] = 0 is an empty slot of the batch, whose row is skipped.
+ *          rope, or NULL for no rotation. q and q_out may both be NULL (then n_q_heads is not read).
+ * Outputs: the pages and scales; q_out [n_tokens, Hq, hd] dense, the rotated queries rounded to
+ *          kv->dtype; q_out = q is allowed where q is dense. Rows of skipped sequences are left alone.
+ * A page that receives tokens belongs to one sequence: two sequences that append to the same page
+ * in one call race on it. A page appears once in its sequence.
+ * Device checks: a sequence whose length or token range is out of bounds is skipped
+ * (LR_DEVERR_LEN; where cu_tokens descends, other sequences may be skipped too), a page id out of
+ * range skips that page's keys and values (LR_DEVERR_PAGE).
+ */
+lr_status lr_kv8_append(const lr_kv8_pages* kv, int32_t n_q_heads, int32_t n_tokens, const int32_t* cu_tokens,
+                        const lr_rope* rope, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, void* q_out, void* ws, size_t ws_bytes,
+                        lr_stream_t stream);
+
+/* Workspace bytes lr_decode_attn_kv8 needs. The answer depends on the current device's SM count. */
+size_t lr_kv8_attn_workspace_bytes(const lr_kv8_pages* kv, int32_t n_q_heads);
+
+/*
+ * lr_decode_attn_kv8 -- one decode step of one layer over the 8-bit paged cache: one query token
+ * per sequence, at the end of it. With S = the tokens max(0, lens[b] - window) .. lens[b] - 1
+ * (window = 0: all), G = Hq / Hkv and h = hq / G,
+ *   o[b, hq]   = sum_{t in S} softmax_t(scale * q[b, hq] . k_t) v_t,
+ *   lse[b, hq] = log sum_{t in S} exp(scale * q[b, hq] . k_t),
+ * k_t and v_t the stored codes times their scales. An empty S gives o = 0 and lse = -inf.
+ * scale <= 0 selects 1/sqrt(hd).
+ * With o_prev and lse_prev, an earlier partial result over other tokens (of lr_decode_attn_lse over
+ * the packed context, or of another call of this one) joins the same softmax:
+ *   lse' = log(exp(lse_prev) + exp(lse)),  o' = exp(lse_prev - lse') o_prev + exp(lse - lse') o;
+ * lse_prev = -inf leaves o_prev out.
+ *
+ * Inputs:  q [B, Hq, hd], Hq a multiple of Hkv with at most 8 query heads per KV head;
+ *          o_prev [B, Hq, hd] and lse_prev [B, Hq] fp32, both or neither.
+ * Outputs: o [B, Hq, hd]; lse [B, Hq] fp32 or NULL. o may be o_prev, lse may be lse_prev.
+ * Device checks: a length out of bounds is clipped to [0, 64 max_pages] (LR_DEVERR_LEN), a page id
+ * out of range leaves that page's tokens out (LR_DEVERR_PAGE).
+ */
+lr_status lr_decode_attn_kv8(const lr_kv8_pages* kv, int32_t n_q_heads, const void* q, int32_t window,
+                             float scale, const void* o_prev, const float* lse_prev, void* o, float* lse,
+                             void* ws, size_t ws_bytes, lr_stream_t stream);
 
 /* ------------------------------------------------------------------ errors, version */
 

@@ -8,6 +8,7 @@
 
 #include "lowram.h"
 #include "lr_common.cuh"
+#include "lr_kv8.h"
 #include "lr_launch.h"
 #include "lr_plan.h"
 
@@ -69,6 +70,38 @@ lr_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
   if (!ws) return fail(LR_ERR_INVALID_ARG, "workspace is NULL");
   if (!aligned(ws, 256)) return fail(LR_ERR_INVALID_ARG, "workspace is not 256-byte aligned");
   if (ws_bytes < need) return fail(LR_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, need);
+  return LR_OK;
+}
+
+int64_t kv8_page_stride(const lr_kv8_pages* kv) {
+  return kv->page_stride ? kv->page_stride : (int64_t)kv->n_kv_heads * LR_BLOCK_TOKENS * kv->head_dim;
+}
+
+lr_status check_kv8(const lr_kv8_pages* kv) {
+  if (!kv) return fail(LR_ERR_INVALID_ARG, "kv is NULL");
+  if (kv->batch < 0) return fail(LR_ERR_INVALID_ARG, "batch must be >= 0");
+  if (kv->n_kv_heads < 1 || kv->head_dim < 1 || kv->n_pages < 1 || kv->max_pages < 1)
+    return fail(LR_ERR_INVALID_ARG, "n_kv_heads, head_dim, n_pages and max_pages must be >= 1");
+  if (kv->dtype != LR_F32 && kv->dtype != LR_BF16) return fail(LR_ERR_INVALID_ARG, "unknown dtype %d", (int)kv->dtype);
+  if (kv->head_dim % 8 || kv->head_dim > 256) return fail(LR_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 and <= 256");
+  if (kv->n_kv_heads > (1 << 20) / kv->head_dim) return fail(LR_ERR_UNSUPPORTED, "key width too large");
+  if (kv->max_pages > INT32_MAX / LR_BLOCK_TOKENS) return fail(LR_ERR_UNSUPPORTED, "max_pages too large");
+  const int64_t dense = (int64_t)kv->n_kv_heads * LR_BLOCK_TOKENS * kv->head_dim;
+  if (kv->page_stride && (kv->page_stride < dense || kv->page_stride % 16))
+    return fail(LR_ERR_INVALID_ARG, "page_stride must be 0 or a multiple of 16 of at least one page's bytes");
+  CHECK_PTR(kv->k_codes, "kv.k_codes");
+  CHECK_PTR(kv->v_codes, "kv.v_codes");
+  CHECK_PTR(kv->k_scale, "kv.k_scale");
+  CHECK_PTR(kv->v_scale, "kv.v_scale");
+  CHECK_PTR(kv->page_table, "kv.page_table");
+  CHECK_PTR(kv->lens, "kv.lens");
+  return LR_OK;
+}
+
+lr_status check_kv8_heads(const lr_kv8_pages* kv, int32_t n_q_heads) {
+  if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads)
+    return fail(LR_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of n_kv_heads");
+  if (n_q_heads / kv->n_kv_heads > 8) return fail(LR_ERR_UNSUPPORTED, "more than 8 query heads per KV head");
   return LR_OK;
 }
 
@@ -141,8 +174,8 @@ struct ResRows {
 lr_status decode_impl(const lr_cache_shape* s, int32_t layer, int32_t n_q_heads, const void* q, const void* A,
                       const void* Bt, const lr_predictor* pred, const int32_t* res_idx, const ResRows& rr,
                       const int32_t* res_blk_ptr, int32_t k, const int32_t* block_list, int32_t n_sel,
-                      const void* tail_K, const void* tail_V, int32_t n_tail, float scale, void* o, void* ws,
-                      size_t ws_bytes, lr_stream_t stream) {
+                      const void* tail_K, const void* tail_V, int32_t n_tail, float scale, void* o, float* lse,
+                      void* ws, size_t ws_bytes, lr_stream_t stream) {
   lr_status st = check_shape(s);
   if (st != LR_OK) return st;
   if (layer < 0 || layer >= s->n_layers) return fail(LR_ERR_INVALID_ARG, "layer %d outside [0, %d)", layer, s->n_layers);
@@ -196,6 +229,7 @@ lr_status decode_impl(const lr_cache_shape* s, int32_t layer, int32_t n_q_heads,
   a.tail_V = n_tail ? tail_V : nullptr;
   a.n_tail = n_tail;
   a.o = o;
+  a.lse = lse;
   a.err = (int*)ws;
   a.partials = (float*)((char*)ws + plan.part_off);
   a.n_split = plan.n_split;
@@ -213,7 +247,7 @@ lr_status lr_decode_attn(const lr_cache_shape* s, int32_t layer, int32_t n_q_hea
                          int32_t k, const int32_t* block_list, int32_t n_sel, float scale, void* o,
                          void* ws, size_t ws_bytes, lr_stream_t stream) {
   return decode_impl(s, layer, n_q_heads, q, A, Bt, pred, res_idx, ResRows{res_val, nullptr, nullptr, nullptr},
-                     res_blk_ptr, k, block_list, n_sel, nullptr, nullptr, 0, scale, o, ws, ws_bytes, stream);
+                     res_blk_ptr, k, block_list, n_sel, nullptr, nullptr, 0, scale, o, nullptr, ws, ws_bytes, stream);
 }
 
 lr_status lr_decode_attn_q2(const lr_cache_shape* s, int32_t layer, int32_t n_q_heads, const void* q,
@@ -224,7 +258,7 @@ lr_status lr_decode_attn_q2(const lr_cache_shape* s, int32_t layer, int32_t n_q_
   if (s && s->head_dim % 4) return fail(LR_ERR_UNSUPPORTED, "2-bit rows need head_dim % 4 == 0");
   if (k > 0) CHECK_PTR(res_codes, "res_codes");
   return decode_impl(s, layer, n_q_heads, q, A, Bt, pred, res_idx, ResRows{nullptr, res_codes, res_lo, res_step},
-                     res_blk_ptr, k, block_list, n_sel, nullptr, nullptr, 0, scale, o, ws, ws_bytes, stream);
+                     res_blk_ptr, k, block_list, n_sel, nullptr, nullptr, 0, scale, o, nullptr, ws, ws_bytes, stream);
 }
 
 lr_status lr_quantize_residuals(const lr_cache_shape* s, int64_t n_rows, const void* res_val, uint8_t* res_codes,
@@ -250,7 +284,17 @@ lr_status lr_decode_attn_tail(const lr_cache_shape* s, int32_t layer, int32_t n_
                               const void* tail_V, int32_t n_tail, float scale, void* o, void* ws,
                               size_t ws_bytes, lr_stream_t stream) {
   return decode_impl(s, layer, n_q_heads, q, A, Bt, pred, res_idx, ResRows{res_val, nullptr, nullptr, nullptr},
-                     res_blk_ptr, k, block_list, n_sel, tail_K, tail_V, n_tail, scale, o, ws, ws_bytes, stream);
+                     res_blk_ptr, k, block_list, n_sel, tail_K, tail_V, n_tail, scale, o, nullptr, ws, ws_bytes, stream);
+}
+
+lr_status lr_decode_attn_lse(const lr_cache_shape* s, int32_t layer, int32_t n_q_heads, const void* q,
+                             const void* A, const void* Bt, const lr_predictor* pred,
+                             const int32_t* res_idx, const void* res_val, const int32_t* res_blk_ptr,
+                             int32_t k, const int32_t* block_list, int32_t n_sel, float scale, void* o,
+                             float* lse, void* ws, size_t ws_bytes, lr_stream_t stream) {
+  CHECK_PTR(lse, "lse");
+  return decode_impl(s, layer, n_q_heads, q, A, Bt, pred, res_idx, ResRows{res_val, nullptr, nullptr, nullptr},
+                     res_blk_ptr, k, block_list, n_sel, nullptr, nullptr, 0, scale, o, lse, ws, ws_bytes, stream);
 }
 
 // ------------------------------------------------------------------ block selection
@@ -447,6 +491,104 @@ lr_status lr_residual_block_ptr(const int32_t* idx, int32_t n_segments, int32_t 
   CHECK_PTR(ptr_out, "ptr_out");
   cudaError_t e = lr::launch_block_ptr(idx, n_segments, k, T, ptr_out, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "block pointer launch");
+  return LR_OK;
+}
+
+// ------------------------------------------------------------------ 8-bit paged cache
+
+size_t lr_kv8_append_workspace_bytes(const lr_kv8_pages* kv) { return check_kv8(kv) == LR_OK ? 256 : 0; }
+
+lr_status lr_kv8_append(const lr_kv8_pages* kv, int32_t n_q_heads, int32_t n_tokens, const int32_t* cu_tokens,
+                        const lr_rope* rope, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                        const void* v, int64_t v_stride, void* q_out, void* ws, size_t ws_bytes,
+                        lr_stream_t stream) {
+  lr_status st = check_kv8(kv);
+  if (st != LR_OK) return st;
+  if (n_tokens < 0) return fail(LR_ERR_INVALID_ARG, "n_tokens must be >= 0");
+  if (!cu_tokens && n_tokens != kv->batch)
+    return fail(LR_ERR_INVALID_ARG, "n_tokens=%d without cu_tokens must be batch=%d", n_tokens, kv->batch);
+  CHECK_OPT_PTR(cu_tokens, "cu_tokens");
+  if ((q != nullptr) != (q_out != nullptr)) return fail(LR_ERR_INVALID_ARG, "q and q_out go together");
+  if (q && (n_q_heads < 1 || n_q_heads > (1 << 20) / kv->head_dim))
+    return fail(LR_ERR_INVALID_ARG, "n_q_heads=%d out of range", n_q_heads);
+  int rot = 0;
+  if (rope) {
+    rot = rope->rot_dim;
+    if (rot < 0 || rot > kv->head_dim) return fail(LR_ERR_INVALID_ARG, "rot_dim=%d outside [0, head_dim]", rot);
+    if (rot % 16) return fail(LR_ERR_UNSUPPORTED, "rot_dim must be a multiple of 16");
+    if (rope->interleaved != 0 && rope->interleaved != 1)
+      return fail(LR_ERR_INVALID_ARG, "rope.interleaved must be 0 or 1");
+    if (rot) CHECK_PTR(rope->inv_freq, "rope.inv_freq");
+  }
+  if (n_tokens > 0) {
+    CHECK_PTR(k, "k");
+    CHECK_PTR(v, "v");
+  }
+  CHECK_OPT_PTR(q, "q");
+  CHECK_OPT_PTR(q_out, "q_out");
+  const int64_t kv_row = (int64_t)kv->n_kv_heads * kv->head_dim, q_row = q ? (int64_t)n_q_heads * kv->head_dim : 0;
+  if (!k_stride) k_stride = kv_row;
+  if (!v_stride) v_stride = kv_row;
+  if (!q_stride) q_stride = q_row;
+  const int64_t unit = kv->dtype == LR_BF16 ? 8 : 4;  // 16 bytes
+  if (k_stride < kv_row || v_stride < kv_row || (q && q_stride < q_row))
+    return fail(LR_ERR_INVALID_ARG, "a token stride is less than a token's row");
+  if (k_stride % unit || v_stride % unit || (q && q_stride % unit))
+    return fail(LR_ERR_INVALID_ARG, "token strides must be whole 16 bytes");
+  if (q && q_out == q && q_stride != q_row) return fail(LR_ERR_INVALID_ARG, "q_out = q needs a dense q");
+  if ((st = check_ws(ws, ws_bytes, 256)) != LR_OK) return st;
+  lr::Kv8AppendArgs a{};
+  a.B = kv->batch; a.Hkv = kv->n_kv_heads; a.Hq = q ? n_q_heads : 0; a.hd = kv->head_dim;
+  a.n_pages = kv->n_pages; a.max_pages = kv->max_pages; a.n_tokens = n_tokens;
+  a.page_stride = kv8_page_stride(kv);
+  a.kc = kv->k_codes; a.vc = kv->v_codes; a.ks = kv->k_scale; a.vs = kv->v_scale;
+  a.table = kv->page_table; a.lens = kv->lens; a.cu = cu_tokens;
+  a.q = q; a.k = k; a.v = v;
+  a.q_stride = q_stride; a.k_stride = k_stride; a.v_stride = v_stride;
+  a.q_out = q_out;
+  a.inv_freq = rot ? rope->inv_freq : nullptr;
+  a.rot = rot;
+  a.interleaved = rot ? rope->interleaved : 0;
+  a.err = (int*)ws;
+  const cudaError_t e = lr::launch_kv8_append(a, kv->dtype, current_sm_count(), (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "append launch");
+  return LR_OK;
+}
+
+size_t lr_kv8_attn_workspace_bytes(const lr_kv8_pages* kv, int32_t n_q_heads) {
+  if (check_kv8(kv) != LR_OK || check_kv8_heads(kv, n_q_heads) != LR_OK) return 0;
+  return lr::plan_kv8_attn(*kv, n_q_heads, current_sm_count()).ws_bytes;
+}
+
+lr_status lr_decode_attn_kv8(const lr_kv8_pages* kv, int32_t n_q_heads, const void* q, int32_t window, float scale,
+                             const void* o_prev, const float* lse_prev, void* o, float* lse, void* ws,
+                             size_t ws_bytes, lr_stream_t stream) {
+  lr_status st = check_kv8(kv);
+  if (st != LR_OK || (st = check_kv8_heads(kv, n_q_heads)) != LR_OK) return st;
+  if (window < 0) return fail(LR_ERR_INVALID_ARG, "window must be >= 0");
+  CHECK_PTR(q, "q");
+  CHECK_PTR(o, "o");
+  CHECK_OPT_PTR(lse, "lse");
+  if ((o_prev != nullptr) != (lse_prev != nullptr)) return fail(LR_ERR_INVALID_ARG, "o_prev and lse_prev go together");
+  CHECK_OPT_PTR(o_prev, "o_prev");
+  CHECK_OPT_PTR(lse_prev, "lse_prev");
+  const lr::Kv8AttnPlan plan = lr::plan_kv8_attn(*kv, n_q_heads, current_sm_count());
+  if ((st = check_ws(ws, ws_bytes, plan.ws_bytes)) != LR_OK) return st;
+  lr::Kv8AttnArgs a{};
+  a.B = kv->batch; a.Hkv = kv->n_kv_heads; a.G = n_q_heads / kv->n_kv_heads; a.hd = kv->head_dim;
+  a.n_pages = kv->n_pages; a.max_pages = kv->max_pages; a.window = window;
+  a.page_stride = kv8_page_stride(kv);
+  a.scale = (scale > 0.f ? scale : 1.0f / sqrtf((float)kv->head_dim)) * 1.4426950408889634f;
+  a.kc = kv->k_codes; a.vc = kv->v_codes; a.ks = kv->k_scale; a.vs = kv->v_scale;
+  a.table = kv->page_table; a.lens = kv->lens;
+  a.q = q; a.o_prev = o_prev; a.lse_prev = lse_prev; a.o = o; a.lse = lse;
+  a.err = (int*)ws;
+  a.count = (unsigned*)((char*)ws + plan.count_off);
+  a.part = (float*)((char*)ws + plan.part_off);
+  a.n_cta = plan.n_cta;
+  a.part_stride = plan.part_stride;
+  const cudaError_t e = lr::launch_kv8_attn(a, plan, kv->dtype, (cudaStream_t)stream);
+  if (e != cudaSuccess) return cuda_fail(e, "8-bit cache attention launch");
   return LR_OK;
 }
 

@@ -70,6 +70,7 @@ struct DecodeArgs {
   const void* tail_V;   // [B, Hkv, n_tail, hd]
   int n_tail;
   void* o;              // [B, Hq, hd]
+  float* lse;           // [B, Hq] log-sum-exp of the scores, or null
   float* partials;      // [B, Hq, n_split, part_stride]
   int n_split;
   int part_stride;      // floats per partial: 4 + hd + H + hd

@@ -1,0 +1,62 @@
+// Launch arguments of the 8-bit paged cache (internal to the library).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "lowram.h"
+
+namespace lr {
+
+struct Kv8AppendArgs {
+  int B, Hkv, Hq, hd, n_pages, max_pages, n_tokens;
+  long long page_stride;  // bytes
+  uint8_t* kc;            // [n_pages] x [Hkv, 64, hd]
+  uint8_t* vc;
+  float* ks;              // [n_pages, Hkv]
+  float* vs;
+  const int* table;       // [B, max_pages]
+  const int* lens;        // [B], the new tokens counted
+  const int* cu;          // [B + 1] or null (one token per sequence)
+  const void* q;          // [n_tokens, Hq, hd] rows q_stride elements apart, or null
+  const void* k;          // [n_tokens, Hkv, hd]
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  void* q_out;            // [n_tokens, Hq, hd] dense
+  const float* inv_freq;  // [rot / 2]
+  int rot, interleaved;
+  int* err;
+};
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, lr_dtype dt, int sm_count, cudaStream_t st);
+
+struct Kv8AttnArgs {
+  int B, Hkv, G, hd, n_pages, max_pages, window;
+  long long page_stride;
+  float scale;            // times log2(e): scores in units of 2^x
+  const uint8_t* kc;
+  const uint8_t* vc;
+  const float* ks;
+  const float* vs;
+  const int* table;
+  const int* lens;
+  const void* q;          // [B, Hq, hd]
+  const void* o_prev;     // [B, Hq, hd] or null
+  const float* lse_prev;  // [B, Hq]
+  void* o;                // [B, Hq, hd]
+  float* lse;             // [B, Hq] or null
+  int* err;
+  unsigned* count;        // [n_cta] pieces of a split segment that are done (zero at the start)
+  float* part;            // [2 n_cta] slots of part_stride floats: acc [G, hd], max [8], sum [8]
+  int n_cta;
+  int part_stride;
+};
+struct Kv8AttnPlan {
+  int n_cta;
+  int part_stride;
+  size_t count_off, part_off, ws_bytes;
+};
+Kv8AttnPlan plan_kv8_attn(const lr_kv8_pages& kv, int n_q_heads, int sm_count);
+cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, const Kv8AttnPlan& plan, lr_dtype dt, cudaStream_t st);
+
+}  // namespace lr

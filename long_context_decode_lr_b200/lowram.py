@@ -21,7 +21,7 @@ LR_F32, LR_BF16 = 0, 1
 LR_BLOCK_TOKENS = 64
 LR_MAX_TAIL = 4096
 LR_DEVERR_BLOCK_RANGE, LR_DEVERR_BLOCK_ORDER, LR_DEVERR_RES_RANGE, LR_DEVERR_RES_ORDER, LR_DEVERR_PTR = 1, 2, 4, 8, 16
-LR_DEVERR_TIMEOUT, LR_DEVERR_LAUNCH = 32, 64
+LR_DEVERR_TIMEOUT, LR_DEVERR_LAUNCH, LR_DEVERR_PAGE, LR_DEVERR_LEN = 32, 64, 128, 256
 
 _DT = {torch.float32: LR_F32, torch.bfloat16: LR_BF16}
 
@@ -53,6 +53,18 @@ class lr_predictor_out(ctypes.Structure):
                 ("W2", ctypes.c_void_p), ("b2", ctypes.c_void_p)]
 
 
+class lr_kv8_pages(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("page_stride", ctypes.c_int64), ("k_codes", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("page_table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p)]
+
+
+class lr_rope(ctypes.Structure):
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
+
 _lib = None
 _P = ctypes.c_void_p
 _I = ctypes.c_int32
@@ -68,6 +80,7 @@ def library() -> ctypes.CDLL:
                                "`python -m long_context_decode_lr_b200.build`")
         lib = ctypes.CDLL(LIB_PATH)
         S, Pr = ctypes.POINTER(lr_cache_shape), ctypes.POINTER(lr_predictor)
+        K8, L = ctypes.POINTER(lr_kv8_pages), ctypes.c_int64
         sig = {
             "lr_pack_workspace_bytes": (_Z, [S, _I]),
             "lr_pack_prefill": (_I, [S, _P, _P, _P, Pr, _I, _P, _P, _P, _P, _P, _P, _Z, _P]),
@@ -90,6 +103,12 @@ def library() -> ctypes.CDLL:
             "lr_topk_workspace_bytes": (_Z, [_I, _I, _I]),
             "lr_topk_tokens": (_I, [_P, _I, _I, _I, _P, _P, _Z, _P]),
             "lr_residual_block_ptr": (_I, [_P, _I, _I, _I, _P, _P]),
+            "lr_decode_attn_lse": (_I, [S, _I, _I, _P, _P, _P, Pr, _P, _P, _P, _I, _P, _I, ctypes.c_float,
+                                        _P, _P, _P, _Z, _P]),
+            "lr_kv8_append_workspace_bytes": (_Z, [K8]),
+            "lr_kv8_append": (_I, [K8, _I, _I, _P, ctypes.POINTER(lr_rope), _P, L, _P, L, _P, L, _P, _P, _Z, _P]),
+            "lr_kv8_attn_workspace_bytes": (_Z, [K8, _I]),
+            "lr_decode_attn_kv8": (_I, [K8, _I, _P, _I, ctypes.c_float, _P, _P, _P, _P, _P, _Z, _P]),
             "lr_get_device_error": (_I, [_P, _P, ctypes.POINTER(_I)]),
             "lr_status_string": (ctypes.c_char_p, [_I]),
             "lr_last_error": (ctypes.c_char_p, []),
@@ -207,6 +226,15 @@ def lr_decode_attn_noalloc(shape, layer, n_q_heads, q, A, Bt, predictor: Predict
         _ptr(o), _stream(stream)))
 
 
+def lr_decode_attn_lse(shape, layer, n_q_heads, q, A, Bt, predictor: Predictor, res_idx, res_val,
+                       res_blk_ptr, k, block_list, n_sel, scale, o, lse, ws, stream=None) -> None:
+    """lr_decode_attn that also returns the log-sum-exp of every query head, lse [B, Hq] fp32."""
+    _check(library().lr_decode_attn_lse(
+        ctypes.byref(shape), layer, n_q_heads, _ptr(q), _ptr(A), _ptr(Bt), ctypes.byref(predictor.c),
+        _ptr(res_idx), _ptr(res_val), _ptr(res_blk_ptr), k, _ptr(block_list), n_sel, float(scale),
+        _ptr(o), _ptr(lse), _ptr(ws), 0 if ws is None else ws.numel() * ws.element_size(), _stream(stream)))
+
+
 def lr_decode_attn_tail(shape, layer, n_q_heads, q, A, Bt, predictor: Predictor, res_idx, res_val,
                         res_blk_ptr, k, block_list, n_sel, tail_K, tail_V, n_tail, scale, o, ws,
                         stream=None) -> None:
@@ -248,6 +276,134 @@ def lr_topk_tokens(err, n_segments, T, k, idx_out, ws, stream=None) -> None:
 
 def lr_residual_block_ptr(idx, n_segments, k, T, ptr_out, stream=None) -> None:
     _check(library().lr_residual_block_ptr(_ptr(idx), n_segments, k, T, _ptr(ptr_out), _stream(stream)))
+
+
+# ---- 8-bit paged cache
+
+
+class Kv8Pages:
+    """An 8-bit paged cache of one layer: holds the tensors alive and exposes the C struct.
+
+    k_codes, v_codes [n_pages, Hkv, 64, hd] uint8 (e4m3 codes; pages dense inside, any equal distance
+    between pages), k_scale, v_scale [n_pages, Hkv] fp32, page_table [B, max_pages] int32, lens [B]
+    int32; dtype is that of q, k, v and o beside the cache."""
+
+    def __init__(self, k_codes, v_codes, k_scale, v_scale, page_table, lens, dtype):
+        self.tensors = (k_codes, v_codes, k_scale, v_scale, page_table, lens)
+        if k_codes.dim() != 4 or k_codes.shape != v_codes.shape or k_codes.shape[2] != LR_BLOCK_TOKENS:
+            raise ValueError("k_codes and v_codes must both be [n_pages, Hkv, 64, hd]")
+        n_pages, hkv, _, hd = k_codes.shape
+        if page_table.dim() != 2 or tuple(lens.shape) != (page_table.shape[0],):
+            raise ValueError("page_table must be [B, max_pages] and lens [B]")
+        if tuple(k_scale.shape) != (n_pages, hkv) or tuple(v_scale.shape) != (n_pages, hkv):
+            raise ValueError("k_scale and v_scale must be [n_pages, Hkv]")
+        want = (torch.uint8, torch.uint8, torch.float32, torch.float32, torch.int32, torch.int32)
+        if tuple(t.dtype for t in self.tensors) != want:
+            raise ValueError("codes must be uint8, scales float32, page_table and lens int32")
+        if any(t.device != k_codes.device for t in self.tensors):
+            raise ValueError("the cache's tensors must live on one device")
+        codes = []
+        for t in (k_codes, v_codes):
+            if not t.is_cuda:
+                raise ValueError("tensor must live on a CUDA device")
+            if n_pages and not t[0].is_contiguous():
+                raise ValueError("a page must be contiguous")
+            codes.append(t.data_ptr() or None)
+        stride = k_codes.stride(0) if n_pages > 1 else 0
+        if n_pages > 1 and v_codes.stride(0) != stride:
+            raise ValueError("k_codes and v_codes must have the same distance between pages")
+        self.device, self.dtype = k_codes.device, dtype
+        self.batch, self.n_kv_heads, self.head_dim = page_table.shape[0], hkv, hd
+        self.c = lr_kv8_pages(self.batch, hkv, hd, n_pages, page_table.shape[1], _DT[dtype], stride, *codes,
+                              _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(lens))
+        self.ref = ctypes.byref(self.c)
+
+    def _rows(self, t, n_rows, n_heads, name):
+        """A [n_rows, n_heads, hd] tensor of the cache's dtype and device."""
+        if t.dtype != self.dtype or t.device != self.device or tuple(t.shape) != (n_rows, n_heads, self.head_dim):
+            raise ValueError(f"{name} must be a {self.dtype} tensor [{n_rows}, {n_heads}, {self.head_dim}] on {self.device}")
+        return t
+
+    def _beside(self, t, dtype, shape, name):
+        if t is not None and (t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape):
+            raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} on {self.device}")
+        return _ptr(t)
+
+    def _call(self, entry, args, ws, stream):
+        """Run an entry point on the cache's device, on its current stream unless one is given."""
+        if ws is not None and ws.device != self.device:
+            raise ValueError(f"the workspace must live on {self.device}")
+        tail = (_ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
+        if torch.cuda.current_device() == self.device.index:
+            _check(entry(*args, *tail, _stream(stream)))
+        else:
+            with torch.cuda.device(self.device):
+                _check(entry(*args, *tail, _stream(stream)))
+
+
+class Rope:
+    """Rotary embedding of the first rot_dim dims: inv_freq [rot_dim / 2] fp32, radians per token."""
+
+    def __init__(self, inv_freq, rot_dim: int, interleaved: bool = False):
+        if inv_freq.dtype != torch.float32 or inv_freq.numel() != rot_dim // 2:
+            raise ValueError("inv_freq must be float32 with rot_dim / 2 entries")
+        self.inv_freq = inv_freq
+        self.c = lr_rope(_ptr(inv_freq), int(rot_dim), int(interleaved))
+        self.ref = ctypes.byref(self.c)
+
+
+def _token_stride(t, name):
+    """Distance between the token rows of a [n, heads, hd] view whose rows are dense (0 for one row)."""
+    n, heads, hd = t.shape
+    if hd > 1 and t.stride(2) != 1 or heads > 1 and t.stride(1) != hd:
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.stride(0) if n > 1 else 0
+
+
+def lr_kv8_append_workspace_bytes(kv: Kv8Pages) -> int:
+    return library().lr_kv8_append_workspace_bytes(kv.ref)
+
+
+def lr_kv8_append(kv: Kv8Pages, k, v, ws, cu_tokens=None, rope: Optional[Rope] = None, q=None, q_out=None,
+                  stream=None) -> None:
+    """New keys and values k, v [n, Hkv, hd] into their pages (kv.lens counts them already), keys and the
+    queries q [n, Hq, hd] -> q_out rotated by position. k, v and q may be slices of one fused tensor.
+    cu_tokens [B + 1] int32 gives each sequence's rows; without it every sequence has one."""
+    n = k.shape[0]
+    kv._rows(k, n, kv.n_kv_heads, "k")
+    kv._rows(v, n, kv.n_kv_heads, "v")
+    hq, q_ptr, q_stride, out_ptr = 0, None, 0, None
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    if q is not None:
+        hq = q.shape[1]
+        q_ptr, q_stride = kv._rows(q, n, hq, "q").data_ptr() or None, _token_stride(q, "q")
+        out_ptr = _ptr(kv._rows(q_out, n, hq, "q_out"))
+    if rope is not None and rope.inv_freq.device != kv.device:
+        raise ValueError(f"inv_freq must live on {kv.device}")
+    cu = kv._beside(cu_tokens, torch.int32, (kv.batch + 1,), "cu_tokens")
+    kv._call(library().lr_kv8_append,
+             (kv.ref, hq, n, cu, None if rope is None else rope.ref, q_ptr, q_stride, k.data_ptr() or None,
+              _token_stride(k, "k"), v.data_ptr() or None, _token_stride(v, "v"), out_ptr), ws, stream)
+
+
+def lr_kv8_attn_workspace_bytes(kv: Kv8Pages, n_q_heads: int) -> int:
+    if torch.cuda.is_available() and torch.cuda.current_device() != kv.device.index:
+        with torch.cuda.device(kv.device):
+            return library().lr_kv8_attn_workspace_bytes(kv.ref, n_q_heads)
+    return library().lr_kv8_attn_workspace_bytes(kv.ref, n_q_heads)
+
+
+def lr_decode_attn_kv8(kv: Kv8Pages, n_q_heads, q, o, ws, lse=None, window=0, scale=0.0, o_prev=None, lse_prev=None,
+                       stream=None) -> None:
+    """One decode step over the 8-bit paged cache: q, o [B, Hq, hd]; lse [B, Hq] fp32 (optional);
+    o_prev, lse_prev: an earlier partial result over other tokens, joined to the same softmax."""
+    b = kv.batch
+    args = (kv.ref, n_q_heads, _ptr(kv._rows(q, b, n_q_heads, "q")), int(window), float(scale),
+            None if o_prev is None else _ptr(kv._rows(o_prev, b, n_q_heads, "o_prev")),
+            kv._beside(lse_prev, torch.float32, (b, n_q_heads), "lse_prev"),
+            _ptr(kv._rows(o, b, n_q_heads, "o")), kv._beside(lse, torch.float32, (b, n_q_heads), "lse"))
+    kv._call(library().lr_decode_attn_kv8, args, ws, stream)
 
 
 def lr_get_device_error(ws, stream=None) -> int:
