@@ -1,5 +1,5 @@
-// Decode attention over the 8-bit paged cache on the CUDA cores: every storage type, head_dim and
-// group size the entry point takes.
+// Decode attention over the 8-bit paged cache: the choice of the kernel, and the kernel on the CUDA
+// cores for every storage type, head_dim and group size the entry point takes.
 //
 // One CTA of 128 threads walks its share of the batch's tiles (kv8_common.cuh), two pages of 64
 // tokens at a time: thread t holds the score of token t for the G query heads of the KV head
@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(NT) kv8_attn_kernel(Kv8AttnArgs a) {
   __shared__ int last;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hd = a.hd, G = a.G;
-  empty_sequences<T, NT>(a);
+  empty_sequences<T>(a, tid, NT);
   Walk k(a, find_work<NT>(a, scratch));
   while (k.next()) {
     const int* table = a.table + (size_t)k.b * a.max_pages;
@@ -215,6 +215,7 @@ Kv8AttnPlan plan_kv8_attn(const lr_kv8_pages& kv, int n_q_heads, int sm_count) {
   Kv8AttnPlan p{};
   const int G = n_q_heads / kv.n_kv_heads;
   const long long most = (long long)kv.batch * kv.n_kv_heads * ((kv.max_pages + 1) / 2);  // tiles
+  p.tensor = kv.dtype == LR_BF16 && kv.head_dim == 128;
   p.n_cta = (int)std::max(1LL, std::min(most, 2LL * sm_count));
   p.part_stride = G * kv.head_dim + 16;
   p.count_off = 256;
@@ -226,6 +227,11 @@ Kv8AttnPlan plan_kv8_attn(const lr_kv8_pages& kv, int n_q_heads, int sm_count) {
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, const Kv8AttnPlan& plan, lr_dtype dt, cudaStream_t st) {
   const cudaError_t e = cudaMemsetAsync(a.err, 0, plan.part_off, st);  // error word and piece counts
   if (e != cudaSuccess || a.B == 0) return e;
+  if (plan.tensor) {
+    CUtensorMap mk, mv;
+    if (!kv8_page_map(&mk, a.kc, a) || !kv8_page_map(&mv, a.vc, a)) return cudaErrorInvalidValue;
+    return kv8::launch_attn_tc(a, mk, mv, st);
+  }
   if (dt == LR_BF16) {
     if (a.hd <= 128) kv8::kv8_attn_kernel<__nv_bfloat16, 1><<<plan.n_cta, kv8::NT, 0, st>>>(a);
     else kv8::kv8_attn_kernel<__nv_bfloat16, 2><<<plan.n_cta, kv8::NT, 0, st>>>(a);

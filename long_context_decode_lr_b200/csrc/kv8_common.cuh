@@ -255,20 +255,21 @@ __device__ __forceinline__ void join_pieces(const Kv8AttnArgs& a, const Pieces& 
 }
 
 // o = 0, lse = -inf (or the earlier partial result) for the sequences without tokens, shared out
-// among the CTAs, and the device checks of the lengths.
-template <typename T, int NT>
-__device__ __forceinline__ void empty_sequences(const Kv8AttnArgs& a) {
+// among the CTAs, and the device checks of the lengths. Called by `threads` threads (whole warps) of
+// the CTA, `tid` counted among them.
+template <typename T>
+__device__ __forceinline__ void empty_sequences(const Kv8AttnArgs& a, int tid, int threads) {
   for (int b = blockIdx.x; b < a.B; b += a.n_cta) {
     const int len = __ldg(a.lens + b);
-    if (threadIdx.x == 0 && (len < 0 || len > a.max_pages * kBlock)) flag_error(a.err, LR_DEVERR_LEN);
+    if (tid == 0 && (len < 0 || len > a.max_pages * kBlock)) flag_error(a.err, LR_DEVERR_LEN);
     if (len > 0) continue;
     const int Hq = a.Hkv * a.G;
-    for (int r = threadIdx.x / 32; r < Hq; r += NT / 32) {
+    for (int r = tid / 32; r < Hq; r += threads / 32) {
       const size_t row = (size_t)b * Hq + r;
       const Joined j = join_prev(a, row, -CUDART_INF_F, 0.f);
-      for (int d = threadIdx.x & 31; d < a.hd; d += 32) ((T*)a.o)[row * a.hd + d] = joined_value<T>(a, row, d, j, 0.f);
+      for (int d = tid & 31; d < a.hd; d += 32) ((T*)a.o)[row * a.hd + d] = joined_value<T>(a, row, d, j, 0.f);
       __syncwarp();
-      if (a.lse && (threadIdx.x & 31) == 0) a.lse[row] = j.lse;
+      if (a.lse && (tid & 31) == 0) a.lse[row] = j.lse;
     }
   }
 }

@@ -1,6 +1,7 @@
 // Launch arguments of the 8-bit paged cache (internal to the library).
 #pragma once
 
+#include <cuda.h>
 #include <cuda_runtime.h>
 #include <stddef.h>
 #include <stdint.h>
@@ -52,11 +53,18 @@ struct Kv8AttnArgs {
   int part_stride;
 };
 struct Kv8AttnPlan {
+  bool tensor;            // the tensor-core kernel (bf16, head_dim 128)
   int n_cta;
   int part_stride;
   size_t count_off, part_off, ws_bytes;
 };
 Kv8AttnPlan plan_kv8_attn(const lr_kv8_pages& kv, int n_q_heads, int sm_count);
+// Tensor map of a pool of pages with head_dim 128, a box one page of one head (plan.cu).
+bool kv8_page_map(CUtensorMap* m, const uint8_t* codes, const Kv8AttnArgs& a);
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, const Kv8AttnPlan& plan, lr_dtype dt, cudaStream_t st);
+
+namespace kv8 {
+cudaError_t launch_attn_tc(const Kv8AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st);
+}
 
 }  // namespace lr

@@ -8,6 +8,7 @@
 #include "lr_plan.h"
 #include "lr_fit.h"
 #include "lr_gemm.h"
+#include "lr_kv8.h"
 #include "lr_tc.h"
 
 namespace lr {
@@ -33,7 +34,7 @@ EncodeTiledFn encode_tiled() {
   return fn;
 }
 
-// A 16-bit tensor map with 128-byte swizzle; dims/box innermost first, out-of-range reads give 0.
+// A tensor map with 128-byte swizzle; dims/box innermost first, out-of-range reads give 0.
 bool tile_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank, const cuuint64_t* dims,
               const cuuint64_t* strides, const cuuint32_t* box) {
   EncodeTiledFn enc = encode_tiled();
@@ -44,6 +45,13 @@ bool tile_map(CUtensorMap* m, CUtensorMapDataType dt, const void* base, int rank
              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 }  // namespace
+
+bool kv8_page_map(CUtensorMap* m, const uint8_t* codes, const Kv8AttnArgs& a) {
+  const cuuint64_t dims[3] = {128, (cuuint64_t)a.Hkv * LR_BLOCK_TOKENS, (cuuint64_t)a.n_pages};
+  const cuuint64_t strides[2] = {128, (cuuint64_t)a.page_stride};
+  const cuuint32_t box[3] = {128, LR_BLOCK_TOKENS, 1};
+  return tile_map(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, codes, 3, dims, strides, box);
+}
 
 bool decode_pair_supported(const lr_cache_shape& s, int n_q_heads) {
   const int G = n_q_heads / s.n_kv_heads;
