@@ -32,10 +32,11 @@ __global__ void __launch_bounds__(NT) kv8_attn_kernel(Kv8AttnArgs a) {
   __shared__ __align__(16) float qs[256][8];   // q * scale, head fastest
   __shared__ __align__(16) float ps[NT][8];    // p * value scale of the tile's tokens
   __shared__ float red[4][8];
-  __shared__ int last;
+  __shared__ int err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hd = a.hd, G = a.G;
-  empty_sequences<T>(a, tid, NT);
+  if (tid == 0) err = 0;
+  grid_dependency();
   Walk k(a, find_work<NT>(a, scratch));
   while (k.next()) {
     const int* table = a.table + (size_t)k.b * a.max_pages;
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(NT) kv8_attn_kernel(Kv8AttnArgs a) {
           id[x] = __ldg(table + p0 + x);
           if ((unsigned)id[x] >= (unsigned)a.n_pages) {
             id[x] = -1;
-            if (tid == 0) flag_error(a.err, LR_DEVERR_PAGE);
+            if (tid == 0) err |= LR_DEVERR_PAGE;
           }
         }
       }
@@ -162,33 +163,20 @@ __global__ void __launch_bounds__(NT) kv8_attn_kernel(Kv8AttnArgs a) {
 #pragma unroll
     for (int g = 0; g < 8; ++g) l[g] = (red[0][g] + red[1][g]) + (red[2][g] + red[3][g]);
 
-    bool write = k.whole();
-    if (!write) {
-      const Pieces pc = pieces_of(k);
-      float* slot = a.part + (size_t)pc.slot(blockIdx.x - pc.c0) * a.part_stride;
+    if (!k.whole()) {
+      float* slot = a.part + (size_t)piece_slot(k) * a.part_stride;
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         if (g >= G) break;
 #pragma unroll
         for (int x = 0; x < MD; ++x)
-          if (tid + x * NT < hd) __stcg(slot + g * hd + tid + x * NT, acc[x][g]);
+          if (tid + x * NT < hd) slot[g * hd + tid + x * NT] = acc[x][g];
         if (tid == 0) {
-          __stcg(slot + G * hd + g, m[g]);
-          __stcg(slot + G * hd + 8 + g, l[g]);
+          slot[G * hd + g] = m[g];
+          slot[G * hd + 8 + g] = l[g];
         }
       }
-      __threadfence();
-      __syncthreads();
-      if (tid == 0) last = atomicAdd(a.count + pc.c0, 1u) == (unsigned)pc.n - 1;
-      __syncthreads();
-      write = last;
-      if (write) {
-        __threadfence();
-#pragma unroll
-        for (int x = 0; x < MD; ++x) join_pieces<8>(a, pc, tid + x * NT, tid + x * NT < hd, acc[x], m, l);
-      }
-    }
-    if (write) {
+    } else {
       Joined j[8];
 #pragma unroll
       for (int g = 0; g < 8; ++g)
@@ -206,6 +194,121 @@ __global__ void __launch_bounds__(NT) kv8_attn_kernel(Kv8AttnArgs a) {
       }
     }
   }
+  if (tid == 0) a.cta_err[blockIdx.x] = err;
+}
+
+// ------------------------------------------------------------------ joining the pieces
+//
+// CTA (c, g): query head g of the segment that the range of CTA c of the attention kernel is the first to start inside
+// of (none, most of the time). Four numbers to a thread, the pieces spread over the rest of the threads,
+// so that all of them are under way at once; the order of the sums is fixed by the threads. The same
+// grid answers the empty sequences, a row to a warp, and collects the device errors. It may be launched
+// while the attention kernel still runs: only lens is read before it has ended.
+
+constexpr int JT = 128;
+constexpr int kMaxCtas = 1024;
+
+template <typename T>
+__global__ void __launch_bounds__(JT) kv8_join_kernel(Kv8AttnArgs a) {
+  __shared__ long long scratch[JT + 4];
+  __shared__ float weight[kMaxCtas];
+  __shared__ float red[2][JT / 32];
+  __shared__ __align__(16) float sums[JT * 4];
+  __shared__ int err;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int c = blockIdx.x, g = blockIdx.y, Hq = a.Hkv * a.G, hd = a.hd;
+  const Work wk = find_work<JT>(a, scratch);
+  Walk k(a, wk);
+  // the first of the CTAs whose range starts inside the segment
+  const bool mine = c > 0 && k.next() && k.tile0 > 0 && wk.total * (c - 1) / wk.active <= k.seg_first;
+  const bool errors = c == 0 && g == 0;
+  if (errors) {
+    if (tid == 0) err = 0;
+    __syncthreads();
+    bool bad = false;
+    for (int b = tid; b < a.B; b += JT) {
+      const int len = __ldg(a.lens + b);
+      bad |= len < 0 || len > a.max_pages * kBlock;
+    }
+    if (bad) atomicOr(&err, LR_DEVERR_LEN);
+  }
+  const long long n_warps = (long long)gridDim.x * gridDim.y * (JT / 32), rows = (long long)a.B * Hq;
+  for (long long row = ((long long)g * gridDim.x + c) * (JT / 32) + warp; row < rows; row += n_warps) {
+    if (__ldg(a.lens + row / Hq) > 0) continue;
+    const Joined j = join_prev(a, row, -CUDART_INF_F, 0.f);
+    for (int d = lane; d < hd; d += 32) ((T*)a.o)[row * hd + d] = joined_value<T>(a, row, d, j, 0.f);
+    __syncwarp();
+    if (a.lse && lane == 0) a.lse[row] = j.lse;
+  }
+  grid_dependency();
+  if (errors) {
+    int bits = 0;
+    for (int i = tid; i < a.n_cta; i += JT) bits |= __ldcg(a.cta_err + i);
+    if (bits) atomicOr(&err, bits);
+    __syncthreads();
+    if (tid == 0) *a.err = err;
+  }
+  if (!mine) return;
+  const Pieces pc = pieces_of(k);
+  const size_t row = ((size_t)k.b * a.Hkv + k.h) * a.G + g;
+  const int n = pc.n, ml = a.G * hd + g;
+  float m = -CUDART_INF_F;
+  for (int i = tid; i < n; i += JT) {
+    const float mi = __ldcg(a.part + (size_t)pc.slot(i) * a.part_stride + ml);
+    weight[i] = mi;
+    m = fmaxf(m, mi);
+  }
+  m = warp_max(m);
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  const float ref = m == -CUDART_INF_F ? 0.f : m;
+  float l = 0.f;
+  for (int i = tid; i < n; i += JT) {
+    const float w = exp2f(weight[i] - ref);
+    weight[i] = w;
+    l = fmaf(w, __ldcg(a.part + (size_t)pc.slot(i) * a.part_stride + ml + 8), l);
+  }
+  l = warp_sum(l);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  const int cols = hd / 4, groups = JT / cols, col = tid % cols, group = tid / cols;
+  if (group < groups) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = group; i < n; i += groups) {
+      const float w = weight[i];
+      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (size_t)pc.slot(i) * a.part_stride + g * hd) + col);
+      s.x = fmaf(w, v.x, s.x);
+      s.y = fmaf(w, v.y, s.y);
+      s.z = fmaf(w, v.z, s.z);
+      s.w = fmaf(w, v.w, s.w);
+    }
+    reinterpret_cast<float4*>(sums)[group * cols + col] = s;
+  }
+  const Joined j = join_prev(a, row, m, l);
+  __syncthreads();  // lse may be lse_prev: every thread has read it
+  for (int d = tid; d < hd; d += JT) {
+    float acc = 0.f;
+    for (int x = 0; x < groups; ++x) acc += sums[x * hd + d];
+    ((T*)a.o)[row * hd + d] = joined_value<T>(a, row, d, j, acc);
+  }
+  if (a.lse && tid == 0) a.lse[row] = j.lse;
+}
+
+template <typename T>
+cudaError_t launch_attn(const Kv8AttnArgs& a, const Kv8AttnPlan& plan, cudaStream_t st) {
+  cudaError_t e;
+  if (plan.tensor) {
+    CUtensorMap mk, mv;
+    if (!kv8_page_map(&mk, a.kc, a) || !kv8_page_map(&mv, a.vc, a)) return cudaErrorInvalidValue;
+    e = launch_attn_tc(a, mk, mv, st);
+  } else {
+    e = launch_overlapped(a.hd <= 128 ? kv8_attn_kernel<T, 1> : kv8_attn_kernel<T, 2>, dim3(plan.n_cta), NT, 0, st, a);
+  }
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(kv8_join_kernel<T>, dim3(plan.n_cta, a.G), JT, 0, st, a);
 }
 
 }  // namespace
@@ -216,30 +319,17 @@ Kv8AttnPlan plan_kv8_attn(const lr_kv8_pages& kv, int n_q_heads, int sm_count) {
   const int G = n_q_heads / kv.n_kv_heads;
   const long long most = (long long)kv.batch * kv.n_kv_heads * ((kv.max_pages + 1) / 2);  // tiles
   p.tensor = kv.dtype == LR_BF16 && kv.head_dim == 128;
-  p.n_cta = (int)std::max(1LL, std::min(most, 2LL * sm_count));
+  p.n_cta = (int)std::max(1LL, std::min<long long>(most, std::min(2 * sm_count, kv8::kMaxCtas)));
   p.part_stride = G * kv.head_dim + 16;
-  p.count_off = 256;
-  p.part_off = (256 + (size_t)p.n_cta * sizeof(unsigned) + 255) & ~(size_t)255;
+  p.cta_err_off = 256;
+  p.part_off = (256 + (size_t)p.n_cta * sizeof(int) + 255) & ~(size_t)255;
   p.ws_bytes = p.part_off + (((size_t)2 * p.n_cta * p.part_stride * sizeof(float) + 255) & ~(size_t)255);
   return p;
 }
 
 cudaError_t launch_kv8_attn(const Kv8AttnArgs& a, const Kv8AttnPlan& plan, lr_dtype dt, cudaStream_t st) {
-  const cudaError_t e = cudaMemsetAsync(a.err, 0, plan.part_off, st);  // error word and piece counts
-  if (e != cudaSuccess || a.B == 0) return e;
-  if (plan.tensor) {
-    CUtensorMap mk, mv;
-    if (!kv8_page_map(&mk, a.kc, a) || !kv8_page_map(&mv, a.vc, a)) return cudaErrorInvalidValue;
-    return kv8::launch_attn_tc(a, mk, mv, st);
-  }
-  if (dt == LR_BF16) {
-    if (a.hd <= 128) kv8::kv8_attn_kernel<__nv_bfloat16, 1><<<plan.n_cta, kv8::NT, 0, st>>>(a);
-    else kv8::kv8_attn_kernel<__nv_bfloat16, 2><<<plan.n_cta, kv8::NT, 0, st>>>(a);
-  } else {
-    if (a.hd <= 128) kv8::kv8_attn_kernel<float, 1><<<plan.n_cta, kv8::NT, 0, st>>>(a);
-    else kv8::kv8_attn_kernel<float, 2><<<plan.n_cta, kv8::NT, 0, st>>>(a);
-  }
-  return cudaGetLastError();
+  if (a.B == 0) return cudaMemsetAsync(a.err, 0, 256, st);
+  return dt == LR_BF16 ? kv8::launch_attn<__nv_bfloat16>(a, plan, st) : kv8::launch_attn<float>(a, plan, st);
 }
 
 }  // namespace lr

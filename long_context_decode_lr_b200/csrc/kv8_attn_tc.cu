@@ -18,8 +18,7 @@
 // threads exchange. Scales and the rescaling between tiles are fp32 factors in registers.
 //
 // Persistent, two CTAs per SM on an even share of the tiles (kv8_common.cuh): warps 0-3 softmax and
-// sums, warp 4 loads (TMA, three stages of 32 KB) and answers empty sequences, warp 5 issues the
-// products. Bound by HBM: 256 bytes per token and KV head against about 2 cycles of the tensor pipe.
+// sums, warp 4 loads (TMA, three stages of 32 KB), warp 5 issues the products. Bound by HBM: 256 bytes per token and KV head against about 2 cycles of the tensor pipe.
 #include <algorithm>
 
 #include "kv8_common.cuh"
@@ -62,11 +61,6 @@ static_assert(2 * (Layout::kBytes + 1024) <= 227 * 1024, "two CTAs per SM");
 enum Bar { K_FULL = 0, V_FULL = K_FULL + kStages, EMPTY = V_FULL + kStages, Q_READY = EMPTY + kStages, S_FULL, P_READY, O_FULL, DRAIN, kBars };
 static_assert(kBars * 8 <= 128, "barriers");
 
-__device__ __forceinline__ float redux_max(float v) {
-  float r;
-  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
-  return r;
-}
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate) {
@@ -87,14 +81,15 @@ struct Shared {
   uint8_t* base;
   __device__ uint64_t* bar(int i) const { return reinterpret_cast<uint64_t*>(base + Layout::kOffBar) + i; }
   __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(base + Layout::kOffMisc + 4); }
+  __device__ int* err() const { return reinterpret_cast<int*>(base + Layout::kOffMisc + 8); }
   __device__ Meta* meta(int s) const { return reinterpret_cast<Meta*>(base + Layout::kOffMeta) + s; }
   __device__ uint8_t* keys(int s) const { return base + Layout::kOffRing + s * 2 * kTileBytes; }
   __device__ uint8_t* values(int s) const { return keys(s) + kTileBytes; }
 };
 
-__device__ __forceinline__ void give_up(const Kv8AttnArgs& a, const Shared& sh) {
+__device__ __forceinline__ void give_up(const Shared& sh) {
   *sh.abort_flag() = 1;
-  flag_error(a.err, LR_DEVERR_TIMEOUT);
+  atomicOr(sh.err(), LR_DEVERR_TIMEOUT);
 }
 
 // ------------------------------------------------------------------ loads (warp 4)
@@ -120,7 +115,7 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
         ks = __ldg(a.ks + (size_t)id * a.Hkv + k.h);
         vs = __ldg(a.vs + (size_t)id * a.Hkv + k.h);
       } else {
-        if (p0 + lane < page_end) flag_error(a.err, LR_DEVERR_PAGE);
+        if (p0 + lane < page_end) atomicOr(sh.err(), LR_DEVERR_PAGE);
         id = -1;
       }
       for (int j = 0; j < 32 && i < k.tile1; j += kTilePages, ++i, ++it) {
@@ -151,7 +146,7 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
     }
   }
   if (!ok && lane == 0) {
-    give_up(a, sh);
+    give_up(sh);
     // nothing may land in shared memory after the CTA has gone
     for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j) {
       mbar_wait_drain(sh.bar(K_FULL + j % kStages), (j / kStages) & 1, kWaitCycles / 4);
@@ -191,7 +186,7 @@ __device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, const Wor
       mma_commit(sh.bar(EMPTY + s));
     }
   }
-  if (!ok) give_up(a, sh);
+  if (!ok) give_up(sh);
   mma_commit(sh.bar(DRAIN));  // every product has completed before shared memory and TMEM go
   mbar_wait_drain(sh.bar(DRAIN), 0, kWaitCycles / 4);
 }
@@ -210,7 +205,7 @@ __device__ __forceinline__ void write_q(const Kv8AttnArgs& a, const Shared& sh, 
     const uint2 u = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)a.q + (row0 + g) * kHd) + lane);
     float x[4] = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                   __uint_as_float(u.y & 0xffff0000u)};
-    const float top = redux_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+    const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
     // 2^e with top / 2^e in [128, 256); tiny heads share the smallest e, whose inverse is finite
     const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 7, -120);
     const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
@@ -240,13 +235,12 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, u
   const uint32_t tm = tmem + ((uint32_t)(warp * 32) << 16);
   float* wmax = reinterpret_cast<float*>(sh.base + Layout::kOffMax);
   const float* qs_at = reinterpret_cast<const float*>(sh.base + Layout::kOffQs);
-  int* last = reinterpret_cast<int*>(sh.base + Layout::kOffMisc + 8);
   const int G = a.G;
   Walk k(a, wk);
   uint32_t it = 0;
   bool ok = true;  // once a wait has failed the rest runs through without waiting: nobody is left at a barrier
   auto wait = [&](int bar, uint32_t parity) {
-    if (ok && !(ok = mbar_wait(sh.bar(bar), parity, sh.abort_flag()))) give_up(a, sh);
+    if (ok && !(ok = mbar_wait(sh.bar(bar), parity, sh.abort_flag()))) give_up(sh);
   };
   while (k.next()) {
     const size_t row0 = ((size_t)k.b * a.Hkv + k.h) * G;
@@ -285,7 +279,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, u
       float* wm = wmax + (it & 1) * 32;
 #pragma unroll
       for (int g = 0; g < MG; ++g) {
-        const float top = redux_max(x[g]);
+        const float top = warp_max(x[g]);
         if (lane == g) wm[warp * 8 + g] = top;
       }
       soft_sync();
@@ -383,30 +377,18 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, u
 #pragma unroll
     for (int g = 0; g < MG; ++g) l[g] = (red[g] + red[8 + g]) + (red[16 + g] + red[24 + g]);
 
-    bool write = k.whole();
-    if (!write) {
-      const Pieces pc = pieces_of(k);
-      float* slot = a.part + (size_t)pc.slot(blockIdx.x - pc.c0) * a.part_stride;
+    if (!k.whole()) {
+      float* slot = a.part + (size_t)piece_slot(k) * a.part_stride;
 #pragma unroll
       for (int g = 0; g < MG; ++g) {
         if (g >= G) break;
-        __stcg(slot + g * kHd + tid, acc[g]);
+        slot[g * kHd + tid] = acc[g];
         if (tid == 0) {
-          __stcg(slot + G * kHd + g, m[g]);
-          __stcg(slot + G * kHd + 8 + g, l[g]);
+          slot[G * kHd + g] = m[g];
+          slot[G * kHd + 8 + g] = l[g];
         }
       }
-      __threadfence();
-      soft_sync();
-      if (tid == 0) *last = atomicAdd(a.count + pc.c0, 1u) == (unsigned)pc.n - 1;
-      soft_sync();
-      write = *last;
-      if (write) {
-        __threadfence();
-        join_pieces<MG>(a, pc, tid, true, acc, m, l);
-      }
-    }
-    if (write) {
+    } else {
       Joined j[MG];
 #pragma unroll
       for (int g = 0; g < MG; ++g)
@@ -427,7 +409,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const Kv8AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
-    if (threadIdx.x == 0) flag_error(a.err, LR_DEVERR_LAUNCH);
+    if (threadIdx.x == 0) a.cta_err[blockIdx.x] = LR_DEVERR_LAUNCH;
     return;
   }
   const Shared sh{smem};
@@ -445,6 +427,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     mbar_init(sh.bar(O_FULL), 1);
     mbar_init(sh.bar(DRAIN), 1);
     *sh.abort_flag() = 0;
+    *sh.err() = 0;
     fence_mbar_init();
   }
   if (warp == 4 && lane == 0) {
@@ -460,6 +443,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     reinterpret_cast<uint4*>(smem + Layout::kOffQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   tc_fence_before();
+  grid_dependency();
   const Work wk = find_work<kThreads>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
@@ -467,8 +451,6 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     attend<MG>(a, sh, wk, tmem);
   } else if (warp == 4) {
     load_tiles(a, sh, &mk, &mv, wk);
-    __syncwarp();
-    empty_sequences<__nv_bfloat16>(a, lane, 32);
   } else if (lane == 0) {
     issue_products<MG>(a, sh, wk, tmem);
   }
@@ -477,14 +459,14 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   __syncthreads();
   tc_fence_after();
   if (warp == 5) tmem_dealloc(tmem, kTmemCols);
+  if (threadIdx.x == 0) a.cta_err[blockIdx.x] = *sh.err();
 }
 
 template <int MG>
 cudaError_t launch(const Kv8AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kv8_attn_tc_kernel<MG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout::kBytes);
   if (e != cudaSuccess) return e;
-  kv8_attn_tc_kernel<MG><<<a.n_cta, kThreads, Layout::kBytes, st>>>(mk, mv, a);
-  return cudaGetLastError();
+  return launch_overlapped(kv8_attn_tc_kernel<MG>, dim3(a.n_cta), kThreads, Layout::kBytes, st, mk, mv, a);
 }
 
 }  // namespace

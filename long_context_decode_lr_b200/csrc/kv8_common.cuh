@@ -26,6 +26,29 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t codes) {
   return __half22float2(*reinterpret_cast<const __half2*>(&h));
 }
 
+// Waits for the grid before in the stream, then lets the next one be launched: what that one reads before
+// its own wait was complete before this grid went on.
+__device__ __forceinline__ void grid_dependency() {
+  asm volatile("griddepcontrol.wait;\n\tgriddepcontrol.launch_dependents;" ::: "memory");
+}
+
+// Launches a kernel that may start while the grid before drains: it waits for that grid (grid_dependency)
+// before it reads what the grid writes.
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // ------------------------------------------------------------------ attention: the division of work
 //
 // A segment is one (sequence, KV head); its tokens are cut into tiles of two pages. The tiles
@@ -33,8 +56,9 @@ __device__ __forceinline__ float2 e4m3x2_value(uint32_t codes) {
 // takes tiles [c W / C, (c + 1) W / C), so ragged lengths cost nothing and one long sequence
 // fills the machine. A CTA's range touches at most two segments that others share: its first
 // and its last one. What it has of those are pieces (unnormalised sums with their maximum) in the
-// slots 2c and 2c + 1; the last CTA to finish a piece of a segment joins all of them in the
-// order of the CTAs, so the result does not depend on which CTA that is.
+// slots 2c and 2c + 1; a second kernel joins a segment's pieces in the order of the CTAs. (Joined by the
+// last CTA to finish instead, one of them was busy for 5 us with 8 pieces and 20 us with 37, its own
+// tiles waiting.)
 
 constexpr int kTilePages = 2;
 constexpr int kTileTokens = kTilePages * kBlock;
@@ -185,93 +209,36 @@ __device__ __forceinline__ T joined_value(const Kv8AttnArgs& a, size_t row, int 
 
 // ---- pieces of a split segment
 
+// The slot of this CTA's piece of the walk's segment.
+__device__ __forceinline__ int piece_slot(const Walk& k) {
+  return 2 * blockIdx.x + (k.wk.begin < k.seg_first ? 1 : 0);
+}
+
 // The CTAs that share a segment, and the slot of each one's piece.
 struct Pieces {
   int c0, n;
-  long long seg_first, total;
-  int active;
-  __device__ int slot(int i) const {
-    const int c = c0 + i;
-    return 2 * c + (total * c / active < seg_first ? 1 : 0);
-  }
+  bool mid;  // the first CTA's range starts before the segment: its piece is its second one
+  __device__ int slot(int i) const { return 2 * (c0 + i) + (i == 0 && mid ? 1 : 0); }
 };
 __device__ __forceinline__ Pieces pieces_of(const Walk& k) {
   Pieces p;
-  p.seg_first = k.seg_first;
-  p.total = k.wk.total;
-  p.active = k.wk.active;
-  p.c0 = cta_of_tile(k.seg_first, p.total, p.active);
-  p.n = cta_of_tile(k.seg_first + k.sp.tiles - 1, p.total, p.active) - p.c0 + 1;
+  const long long total = k.wk.total;
+  const int active = k.wk.active;
+  p.c0 = cta_of_tile(k.seg_first, total, active);
+  p.n = cta_of_tile(k.seg_first + k.sp.tiles - 1, total, active) - p.c0 + 1;
+  p.mid = total * p.c0 / active < k.seg_first;
   return p;
 }
 
+// Maximum over the warp; a NaN counts only where every lane has one.
 __device__ __forceinline__ float warp_max(float v) {
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  return v;
+  float r;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
+  return r;
 }
 __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
-}
-
-// Sums the pieces in the order of the CTAs, 32 at a time: lane i of every warp weighs piece i, the
-// thread adds up column d of the accumulators. All lanes of a warp call it together.
-template <int MG>
-__device__ __forceinline__ void join_pieces(const Kv8AttnArgs& a, const Pieces& pc, int d, bool has_d, float (&acc)[MG],
-                                            float (&m)[MG], float (&l)[MG]) {
-  const int lane = threadIdx.x & 31;
-#pragma unroll
-  for (int g = 0; g < MG; ++g) {
-    acc[g] = l[g] = 0.f;
-    m[g] = -CUDART_INF_F;
-  }
-  for (int i0 = 0; i0 < pc.n; i0 += 32) {
-    const int n = min(32, pc.n - i0);
-    const float* mine = a.part + (size_t)pc.slot(i0 + min(lane, n - 1)) * a.part_stride;
-    float w[MG];
-#pragma unroll
-    for (int g = 0; g < MG; ++g) {
-      if (g >= a.G) break;
-      const float mi = lane < n ? __ldcg(mine + a.G * a.hd + g) : -CUDART_INF_F;
-      const float li = lane < n ? __ldcg(mine + a.G * a.hd + 8 + g) : 0.f;
-      const float top = fmaxf(m[g], warp_max(mi));
-      const float ref = top == -CUDART_INF_F ? 0.f : top;
-      const float old = exp2f(m[g] - ref);
-      w[g] = exp2f(mi - ref);
-      l[g] = fmaf(l[g], old, warp_sum(li * w[g]));
-      acc[g] *= old;
-      m[g] = top;
-    }
-    for (int i = 0; i < n; ++i) {
-      const float* from = a.part + (size_t)pc.slot(i0 + i) * a.part_stride + d;
-#pragma unroll
-      for (int g = 0; g < MG; ++g) {
-        if (g >= a.G) break;
-        const float wi = __shfl_sync(0xffffffffu, w[g], i);
-        if (has_d) acc[g] = fmaf(wi, __ldcg(from + g * a.hd), acc[g]);
-      }
-    }
-  }
-}
-
-// o = 0, lse = -inf (or the earlier partial result) for the sequences without tokens, shared out
-// among the CTAs, and the device checks of the lengths. Called by `threads` threads (whole warps) of
-// the CTA, `tid` counted among them.
-template <typename T>
-__device__ __forceinline__ void empty_sequences(const Kv8AttnArgs& a, int tid, int threads) {
-  for (int b = blockIdx.x; b < a.B; b += a.n_cta) {
-    const int len = __ldg(a.lens + b);
-    if (tid == 0 && (len < 0 || len > a.max_pages * kBlock)) flag_error(a.err, LR_DEVERR_LEN);
-    if (len > 0) continue;
-    const int Hq = a.Hkv * a.G;
-    for (int r = tid / 32; r < Hq; r += threads / 32) {
-      const size_t row = (size_t)b * Hq + r;
-      const Joined j = join_prev(a, row, -CUDART_INF_F, 0.f);
-      for (int d = tid & 31; d < a.hd; d += 32) ((T*)a.o)[row * a.hd + d] = joined_value<T>(a, row, d, j, 0.f);
-      __syncwarp();
-      if (a.lse && (tid & 31) == 0) a.lse[row] = j.lse;
-    }
-  }
 }
 
 }  // namespace kv8

@@ -47,7 +47,7 @@ struct Kv8AttnArgs {
   void* o;                // [B, Hq, hd]
   float* lse;             // [B, Hq] or null
   int* err;
-  unsigned* count;        // [n_cta] pieces of a split segment that are done (zero at the start)
+  int* cta_err;           // [n_cta] device error bits of each CTA, joined into *err
   float* part;            // [2 n_cta] slots of part_stride floats: acc [G, hd], max [8], sum [8]
   int n_cta;
   int part_stride;
@@ -56,7 +56,7 @@ struct Kv8AttnPlan {
   bool tensor;            // the tensor-core kernel (bf16, head_dim 128)
   int n_cta;
   int part_stride;
-  size_t count_off, part_off, ws_bytes;
+  size_t cta_err_off, part_off, ws_bytes;
 };
 Kv8AttnPlan plan_kv8_attn(const lr_kv8_pages& kv, int n_q_heads, int sm_count);
 // Tensor map of a pool of pages with head_dim 128, a box one page of one head (plan.cu).
