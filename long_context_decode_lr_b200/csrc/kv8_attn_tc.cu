@@ -32,7 +32,7 @@ using namespace sm100;
 
 constexpr int kHd = 128;
 constexpr int kThreads = 192, kSoft = 128;
-constexpr int kStages = 3;
+constexpr int kStages = 3, kQBufs = 4;
 constexpr int kPageBytes = kBlock * kHd;
 constexpr int kTileBytes = kTilePages * kPageBytes;  // of K, and of V
 constexpr int kTmemCols = 128, kColS = 0, kColO = 32;
@@ -45,21 +45,21 @@ struct Meta {  // of a stage's two pages
 
 struct Layout {
   static constexpr int kOffRing = 0;  // stages of K, V
-  static constexpr int kOffQ = kStages * 2 * kTileBytes;  // 16 rows of 128 bytes
-  static constexpr int kOffP = kOffQ + 2048;              // [2][128 tokens][16 bytes]
+  static constexpr int kOffQ = kStages * 2 * kTileBytes;  // [kQBufs] of 16 rows of 128 bytes
+  static constexpr int kOffP = kOffQ + kQBufs * 2048;     // [2][128 tokens][16 bytes]
   static constexpr int kOffMeta = kOffP + 4096;
   static constexpr int kOffMax = kOffMeta + kStages * (int)sizeof(Meta);  // [2][4 warps][8]
-  static constexpr int kOffQs = kOffMax + 2 * 4 * 8 * 4;                  // [8]
-  static constexpr int kOffBar = kOffQs + 32;
-  static constexpr int kOffMisc = kOffBar + 128;
+  static constexpr int kOffQs = kOffMax + 2 * 4 * 8 * 4;                  // [kQBufs][8]
+  static constexpr int kOffBar = kOffQs + kQBufs * 32;
+  static constexpr int kOffMisc = kOffBar + 192;
   static constexpr int kOffScratch = kOffMisc + 16;                       // find_work
   static constexpr int kBytes = kOffScratch + (kThreads + 4) * 8;
 };
 static_assert(Layout::kOffMeta % 16 == 0 && Layout::kOffBar % 8 == 0 && Layout::kOffScratch % 8 == 0, "alignment");
 static_assert(2 * (Layout::kBytes + 1024) <= 227 * 1024, "two CTAs per SM");
 
-enum Bar { K_FULL = 0, V_FULL = K_FULL + kStages, EMPTY = V_FULL + kStages, Q_READY = EMPTY + kStages, S_FULL, P_READY, O_FULL, DRAIN, kBars };
-static_assert(kBars * 8 <= 128, "barriers");
+enum Bar { K_FULL = 0, V_FULL = K_FULL + kStages, EMPTY = V_FULL + kStages, Q_READY = EMPTY + kStages, Q_FREE = Q_READY + kQBufs, S_FULL = Q_FREE + kQBufs, P_READY, O_FULL, DRAIN, kBars };
+static_assert(kBars * 8 <= 192, "barriers");
 
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
 
@@ -83,6 +83,8 @@ struct Shared {
   __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(base + Layout::kOffMisc + 4); }
   __device__ int* err() const { return reinterpret_cast<int*>(base + Layout::kOffMisc + 8); }
   __device__ Meta* meta(int s) const { return reinterpret_cast<Meta*>(base + Layout::kOffMeta) + s; }
+  __device__ uint8_t* queries(int i) const { return base + Layout::kOffQ + i * 2048; }
+  __device__ float* factors(int i) const { return reinterpret_cast<float*>(base + Layout::kOffQs) + i * 8; }
   __device__ uint8_t* keys(int s) const { return base + Layout::kOffRing + s * 2 * kTileBytes; }
   __device__ uint8_t* values(int s) const { return keys(s) + kTileBytes; }
 };
@@ -93,15 +95,50 @@ __device__ __forceinline__ void give_up(const Shared& sh) {
 }
 
 // ------------------------------------------------------------------ loads (warp 4)
-//
+
+// The query heads as two e4m3 terms each: rows g and 8 + g of the K-major operand, and the factors
+// that scores are multiplied by. A head with an infinite number gets a NaN factor. u: dims 4 lane .. 4 lane + 3 of
+// every head, bf16.
+template <int MG>
+__device__ __forceinline__ void write_q(const Kv8AttnArgs& a, const uint2 (&u)[MG], uint8_t* q, float* factor) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int g = 0; g < MG; ++g) {
+    if (g >= a.G) break;
+    float x[4] = {__uint_as_float(u[g].x << 16), __uint_as_float(u[g].x & 0xffff0000u), __uint_as_float(u[g].y << 16),
+                  __uint_as_float(u[g].y & 0xffff0000u)};
+    const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
+    // 2^e with top / 2^e in [128, 256); tiny heads share the smallest e, whose inverse is finite
+    const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 7, -120);
+    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) x[i] *= inv;
+    const uint32_t t1 = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
+    const float2 v0 = e4m3x2_value(t1 & 0xffffu), v1 = e4m3x2_value(t1 >> 16);
+    const uint32_t t2 = e4m3x2((x[0] - v0.x) * 32.f, (x[1] - v0.y) * 32.f) |
+                        (e4m3x2((x[2] - v1.x) * 32.f, (x[3] - v1.y) * 32.f) << 16);
+    const int at = (((lane >> 2) ^ (g & 7)) << 4) + (lane & 3) * 4;  // 128-byte swizzle
+    *reinterpret_cast<uint32_t*>(q + g * 128 + at) = t1;
+    *reinterpret_cast<uint32_t*>(q + (8 + g) * 128 + at) = t2;
+    if (lane == 0) factor[g] = top < CUDART_INF_F ? __uint_as_float((uint32_t)(127 + e) << 23) * a.scale : CUDART_NAN_F;
+  }
+}
+
 // A batch is 32 pages: lane i has the id and the scales of page i. The next batch's ids are under
-// way while one is loaded.
+// way while one is loaded. A segment's queries follow its first tile, up to four segments ahead of the
+// products, so that short sequences do not wait for them.
+template <int MG>
 __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtensorMap* mk, const CUtensorMap* mv, const Work& wk) {
   const int lane = threadIdx.x & 31;
   Walk k(a, wk);
-  uint32_t it = 0;
+  uint32_t it = 0, seg = 0;
   bool ok = true;
-  while (ok && k.next()) {
+  for (; ok && k.next(); ++seg) {
+    uint2 q[MG];
+#pragma unroll
+    for (int g = 0; g < MG; ++g)
+      if (g < a.G)
+        q[g] = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)a.q + (((size_t)k.b * a.Hkv + k.h) * a.G + g) * kHd) + lane);
     const int* table = a.table + (size_t)k.b * a.max_pages;
     const int page_end = min(k.sp.page0 + k.tile1 * kTilePages, (k.sp.n + kBlock - 1) / kBlock);
     auto page_id = [&](int p) { return p < page_end ? __ldg(table + p) : -1; };
@@ -142,6 +179,17 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
           *sh.meta(s) = m;
           mbar_arrive(sh.bar(K_FULL + s));
         }
+        if (i == k.tile0) {
+          const uint32_t buf = seg % kQBufs;
+          if (!(ok = __all_sync(0xffffffffu, mbar_wait(sh.bar(Q_FREE + buf), ((seg / kQBufs) & 1) ^ 1, sh.abort_flag())))) {
+            ++it;  // its loads are under way
+            break;
+          }
+          write_q<MG>(a, q, sh.queries(buf), sh.factors(buf));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sh.bar(Q_READY + buf));
+        }
       }
     }
   }
@@ -160,12 +208,13 @@ template <int MG>
 __device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, uint32_t tmem) {
   constexpr int NP = MG <= 4 ? 16 : 32;
   const uint32_t id_s = idesc_e4m3_f32(128, 16, false, false), id_o = idesc_e4m3_f32(128, NP, true, true);
-  const uint32_t q = smem_u32(sh.base + Layout::kOffQ), p = smem_u32(sh.base + Layout::kOffP);
+  const uint32_t p = smem_u32(sh.base + Layout::kOffP);
   Walk k(a, wk);
   uint32_t it = 0, seg = 0;
   bool ok = true;
   for (; ok && k.next(); ++seg) {
-    ok = mbar_wait(sh.bar(Q_READY), seg & 1, sh.abort_flag());
+    const uint32_t buf = seg % kQBufs, q = smem_u32(sh.queries(buf));
+    ok = mbar_wait(sh.bar(Q_READY + buf), (seg / kQBufs) & 1, sh.abort_flag());
     for (int i = k.tile0; ok && i < k.tile1; ++i, ++it) {
       const uint32_t s = it % kStages, ph = (it / kStages) & 1;
       if (!(ok = mbar_wait(sh.bar(K_FULL + s), ph, sh.abort_flag()))) break;
@@ -193,65 +242,27 @@ __device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, const Wor
 
 // ------------------------------------------------------------------ softmax and sums (warps 0-3)
 
-// The query heads as two e4m3 terms each: rows g and 8 + g of the K-major operand, and the factors
-// that scores are multiplied by. A head with an infinite number gets a NaN factor.
-template <int MG>
-__device__ __forceinline__ void write_q(const Kv8AttnArgs& a, const Shared& sh, size_t row0) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  uint8_t* q = sh.base + Layout::kOffQ;
-#pragma unroll
-  for (int g = warp; g < MG; g += 4) {
-    if (g >= a.G) break;
-    const uint2 u = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)a.q + (row0 + g) * kHd) + lane);
-    float x[4] = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                  __uint_as_float(u.y & 0xffff0000u)};
-    const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
-    // 2^e with top / 2^e in [128, 256); tiny heads share the smallest e, whose inverse is finite
-    const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 7, -120);
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);
-    float r[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) x[i] *= inv;
-    const uint32_t t1 = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
-    const float2 v0 = e4m3x2_value(t1 & 0xffffu), v1 = e4m3x2_value(t1 >> 16);
-    r[0] = (x[0] - v0.x) * 32.f;
-    r[1] = (x[1] - v0.y) * 32.f;
-    r[2] = (x[2] - v1.x) * 32.f;
-    r[3] = (x[3] - v1.y) * 32.f;
-    const uint32_t t2 = e4m3x2(r[0], r[1]) | (e4m3x2(r[2], r[3]) << 16);
-    const int at = (((lane >> 2) ^ (g & 7)) << 4) + (lane & 3) * 4;  // 128-byte swizzle
-    *reinterpret_cast<uint32_t*>(q + g * 128 + at) = t1;
-    *reinterpret_cast<uint32_t*>(q + (8 + g) * 128 + at) = t2;
-    if (lane == 0)
-      reinterpret_cast<float*>(sh.base + Layout::kOffQs)[g] =
-          top < CUDART_INF_F ? __uint_as_float((uint32_t)(127 + e) << 23) * a.scale : CUDART_NAN_F;
-  }
-}
-
 template <int MG>
 __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, uint32_t tmem) {
   constexpr int NP = MG <= 4 ? 16 : 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t tm = tmem + ((uint32_t)(warp * 32) << 16);
   float* wmax = reinterpret_cast<float*>(sh.base + Layout::kOffMax);
-  const float* qs_at = reinterpret_cast<const float*>(sh.base + Layout::kOffQs);
   const int G = a.G;
   Walk k(a, wk);
-  uint32_t it = 0;
+  uint32_t it = 0, seg = 0;
   bool ok = true;  // once a wait has failed the rest runs through without waiting: nobody is left at a barrier
   auto wait = [&](int bar, uint32_t parity) {
     if (ok && !(ok = mbar_wait(sh.bar(bar), parity, sh.abort_flag()))) give_up(sh);
   };
-  while (k.next()) {
+  for (; k.next(); ++seg) {
     const size_t row0 = ((size_t)k.b * a.Hkv + k.h) * G;
-    write_q<MG>(a, sh, row0);  // the products of the last segment are done: their sums have been read
-    fence_proxy_async_smem();
-    soft_sync();
-    if (tid == 0) mbar_arrive(sh.bar(Q_READY));
+    const uint32_t buf = seg % kQBufs;
+    wait(Q_READY + buf, (seg / kQBufs) & 1);
     float qs[MG], m[MG], l[MG], acc[MG];
 #pragma unroll
     for (int g = 0; g < MG; ++g) {
-      qs[g] = g < G ? qs_at[g] : 0.f;
+      qs[g] = g < G ? sh.factors(buf)[g] : 0.f;
       m[g] = -CUDART_INF_F;
       l[g] = acc[g] = 0.f;
     }
@@ -368,6 +379,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, u
     // the sums of p are spread over the threads
     float* red = wmax;
     soft_sync();
+    if (tid == 0) mbar_arrive(sh.bar(Q_FREE + buf));
 #pragma unroll
     for (int g = 0; g < MG; ++g) {
       const float v = warp_sum(l[g]);
@@ -421,7 +433,10 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       mbar_init(sh.bar(V_FULL + i), 1);
       mbar_init(sh.bar(EMPTY + i), 1);
     }
-    mbar_init(sh.bar(Q_READY), 1);
+    for (int i = 0; i < kQBufs; ++i) {
+      mbar_init(sh.bar(Q_READY + i), 1);
+      mbar_init(sh.bar(Q_FREE + i), 1);
+    }
     mbar_init(sh.bar(S_FULL), 1);
     mbar_init(sh.bar(P_READY), kSoft / 32);
     mbar_init(sh.bar(O_FULL), 1);
@@ -439,7 +454,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     tmem_relinquish();
   }
   // rows of absent query heads stay zero
-  for (int i = threadIdx.x; i < 2048 / 16; i += kThreads)
+  for (int i = threadIdx.x; i < kQBufs * 2048 / 16; i += kThreads)
     reinterpret_cast<uint4*>(smem + Layout::kOffQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   tc_fence_before();
@@ -450,7 +465,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   if (warp < 4) {
     attend<MG>(a, sh, wk, tmem);
   } else if (warp == 4) {
-    load_tiles(a, sh, &mk, &mv, wk);
+    load_tiles<MG>(a, sh, &mk, &mv, wk);
   } else if (lane == 0) {
     issue_products<MG>(a, sh, wk, tmem);
   }
