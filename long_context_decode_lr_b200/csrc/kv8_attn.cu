@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(NT) kv8_attn_kernel(Kv8AttnArgs a) {
     for (int g = 0; g < 8; ++g) l[g] = (red[0][g] + red[1][g]) + (red[2][g] + red[3][g]);
 
     if (!k.whole()) {
-      float* slot = a.part + (size_t)piece_slot(k) * a.part_stride;
+      float* slot = a.part + (size_t)piece_slot(k.wk, k.seg_first) * a.part_stride;
 #pragma unroll
       for (int g = 0; g < 8; ++g) {
         if (g >= G) break;

@@ -32,36 +32,55 @@ using namespace sm100;
 
 constexpr int kHd = 128;
 constexpr int kThreads = 192, kSoft = 128;
-constexpr int kStages = 3, kQBufs = 4;
+constexpr int kStages = 3;
 constexpr int kPageBytes = kBlock * kHd;
 constexpr int kTileBytes = kTilePages * kPageBytes;  // of K, and of V
 constexpr int kTmemCols = 128, kColS = 0, kColO = 32;
 
-struct Meta {  // of a stage's two pages
-  float ks[2], vs[2];
-  int ok[2];
+// What the loading warp says of the tile in a stage.
+enum Flag { OK0 = 1, OK1 = 2, FIRST = 4, LAST = 8, WHOLE = 16, END = 32 };
+struct __align__(16) Meta {
+  float ks[2], vs[2];    // scales of its two pages
+  int t0, lo, n, flags;  // its first token, the attended ones; which pages there are (OK0, OK1), first or last
+                         // tile of the segment here, all of the segment here, no tile: the end
+  int seg, slot;         // b * Hkv + h, and where a piece of it goes
   int pad[2];
 };
 
 struct Layout {
-  static constexpr int kOffRing = 0;  // stages of K, V
-  static constexpr int kOffQ = kStages * 2 * kTileBytes;  // [kQBufs] of 16 rows of 128 bytes
-  static constexpr int kOffP = kOffQ + kQBufs * 2048;     // [2][128 tokens][16 bytes]
-  static constexpr int kOffMeta = kOffP + 4096;
+  static constexpr int kOffRing = 0;                         // stages of K, V
+  static constexpr int kOffQ = kStages * 2 * kTileBytes;     // 16 rows of 128 bytes
+  static constexpr int kOffP = kOffQ + 2048;                 // [2][128 tokens][16 bytes]
+  static constexpr int kOffRawQ = kOffP + 4096;              // [kStages][8][128] bf16
+  static constexpr int kOffMeta = kOffRawQ + kStages * 2048;
   static constexpr int kOffMax = kOffMeta + kStages * (int)sizeof(Meta);  // [2][4 warps][8]
-  static constexpr int kOffQs = kOffMax + 2 * 4 * 8 * 4;                  // [kQBufs][8]
-  static constexpr int kOffBar = kOffQs + kQBufs * 32;
-  static constexpr int kOffMisc = kOffBar + 192;
+  static constexpr int kOffRed = kOffMax + 2 * 4 * 8 * 4;    // [4 warps][8]
+  static constexpr int kOffQs = kOffRed + 4 * 8 * 4;         // [8]
+  static constexpr int kOffBar = kOffQs + 32;
+  static constexpr int kOffMisc = kOffBar + 128;
   static constexpr int kOffScratch = kOffMisc + 16;                       // find_work
   static constexpr int kBytes = kOffScratch + (kThreads + 4) * 8;
 };
 static_assert(Layout::kOffMeta % 16 == 0 && Layout::kOffBar % 8 == 0 && Layout::kOffScratch % 8 == 0, "alignment");
 static_assert(2 * (Layout::kBytes + 1024) <= 227 * 1024, "two CTAs per SM");
 
-enum Bar { K_FULL = 0, V_FULL = K_FULL + kStages, EMPTY = V_FULL + kStages, Q_READY = EMPTY + kStages, Q_FREE = Q_READY + kQBufs, S_FULL = Q_FREE + kQBufs, P_READY, O_FULL, DRAIN, kBars };
-static_assert(kBars * 8 <= 192, "barriers");
+enum Bar { K_FULL = 0, V_FULL = K_FULL + kStages, EMPTY = V_FULL + kStages, Q_READY = EMPTY + kStages, S_FULL, P_READY, O_FULL, DRAIN, kBars };
+static_assert(kBars * 8 <= 128, "barriers");
 
+// Barriers of the softmax warps; soft_all also says whether `ok` held in all of them.
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
+__device__ __forceinline__ bool soft_all(bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "bar.red.and.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)ok), "n"(kSoft)
+      : "memory");
+  return r != 0;
+}
 
 __device__ __forceinline__ void mma_e4m3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, bool accumulate) {
   asm volatile(
@@ -83,8 +102,9 @@ struct Shared {
   __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(base + Layout::kOffMisc + 4); }
   __device__ int* err() const { return reinterpret_cast<int*>(base + Layout::kOffMisc + 8); }
   __device__ Meta* meta(int s) const { return reinterpret_cast<Meta*>(base + Layout::kOffMeta) + s; }
-  __device__ uint8_t* queries(int i) const { return base + Layout::kOffQ + i * 2048; }
-  __device__ float* factors(int i) const { return reinterpret_cast<float*>(base + Layout::kOffQs) + i * 8; }
+  __device__ uint8_t* queries() const { return base + Layout::kOffQ; }
+  __device__ uint8_t* raw_queries(int s) const { return base + Layout::kOffRawQ + s * 2048; }
+  __device__ float* factors() const { return reinterpret_cast<float*>(base + Layout::kOffQs); }
   __device__ uint8_t* keys(int s) const { return base + Layout::kOffRing + s * 2 * kTileBytes; }
   __device__ uint8_t* values(int s) const { return keys(s) + kTileBytes; }
 };
@@ -95,18 +115,128 @@ __device__ __forceinline__ void give_up(const Shared& sh) {
 }
 
 // ------------------------------------------------------------------ loads (warp 4)
+//
+// The CTA's units are taken 16 at a time: lanes 2j and 2j + 1 find the segment of unit j and have the ids
+// and scales of its two pages, and lane 2j issues the loads of the tile. While one batch is loaded the ids
+// and then the scales of the next are on their way, whatever segments they belong to.
+
+struct Batch {
+  Place at;
+  int id;        // this lane's page, -1: none
+  bool live;     // there is a tile
+  bool page;     // and this page of it
+  float ks, vs;
+};
+
+__device__ __forceinline__ void batch_ids(const Kv8AttnArgs& a, const Work& wk, long long unit, Batch& t) {
+  t.live = t.page = false;
+  t.id = -1;
+  if (unit >= wk.end) return;
+  t.at.seek(a, unit);
+  t.live = t.at.tile < t.at.sp.tiles;
+  const int p = t.at.sp.page0 + t.at.tile * kTilePages + (int)(threadIdx.x & 1);
+  t.page = t.live && p * kBlock < t.at.sp.n;
+  if (t.page) t.id = __ldg(a.table + (size_t)t.at.b * a.max_pages + p);
+}
+__device__ __forceinline__ void batch_scales(const Kv8AttnArgs& a, const Shared& sh, Batch& t) {
+  t.ks = t.vs = 0.f;
+  if ((unsigned)t.id < (unsigned)a.n_pages) {
+    t.ks = __ldg(a.ks + (size_t)t.id * a.Hkv + t.at.h);
+    t.vs = __ldg(a.vs + (size_t)t.id * a.Hkv + t.at.h);
+  } else {
+    if (t.page) atomicOr(sh.err(), LR_DEVERR_PAGE);
+    t.id = -1;
+  }
+}
+
+__device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtensorMap* mk, const CUtensorMap* mv, const Work& wk) {
+  const int lane = threadIdx.x & 31;
+  uint32_t it = 0;
+  bool ok = true;
+  Batch next;
+  long long unit = wk.begin + (lane >> 1);  // of this lane, in the batch under way
+  if (wk.begin < wk.end) next.at.start(a, wk);
+  batch_ids(a, wk, unit, next);
+  batch_scales(a, sh, next);
+  while (ok && unit - (lane >> 1) < wk.end) {
+    const Batch t = next;
+    const int id1 = __shfl_xor_sync(0xffffffffu, t.id, 1);
+    const float ks1 = __shfl_xor_sync(0xffffffffu, t.ks, 1), vs1 = __shfl_xor_sync(0xffffffffu, t.vs, 1);
+    uint32_t live = __ballot_sync(0xffffffffu, t.live) & 0x55555555u;
+    batch_ids(a, wk, unit + 16, next);
+    for (int x = 0; x < 16; ++x) {
+      if (x == 8) batch_scales(a, sh, next);
+      if (!live) continue;
+      const int src = __ffs(live) - 1;
+      live &= live - 1;
+      const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+      if (!(ok = __all_sync(0xffffffffu, mbar_wait(sh.bar(EMPTY + s), ph ^ 1, sh.abort_flag())))) break;
+      ++it;
+      if (lane == src) {
+        const bool first = t.at.tile == 0 || unit == wk.begin;
+        const bool last = t.at.tile == t.at.sp.tiles - 1 || unit == wk.end - 1;
+        const int seg = t.at.b * a.Hkv + t.at.h, row = t.at.h * kBlock;
+        const uint32_t bytes = ((t.id >= 0) + (id1 >= 0)) * kPageBytes, q_bytes = a.G * kHd * 2;
+        uint64_t *kf = sh.bar(K_FULL + s), *vf = sh.bar(V_FULL + s);
+        mbar_arrive_expect_tx(kf, bytes + (first ? q_bytes : 0));
+        if (t.id >= 0) tma_load_3d(sh.keys(s), mk, kf, 0, row, t.id);
+        if (id1 >= 0) tma_load_3d(sh.keys(s) + kPageBytes, mk, kf, 0, row, id1);
+        if (first) bulk_load(sh.raw_queries(s), (const __nv_bfloat16*)a.q + (size_t)seg * a.G * kHd, q_bytes, kf);
+        mbar_arrive_expect_tx(vf, bytes);
+        if (t.id >= 0) tma_load_3d(sh.values(s), mv, vf, 0, row, t.id);
+        if (id1 >= 0) tma_load_3d(sh.values(s) + kPageBytes, mv, vf, 0, row, id1);
+        Meta m;
+        m.ks[0] = t.ks;
+        m.ks[1] = ks1;
+        m.vs[0] = t.vs;
+        m.vs[1] = vs1;
+        m.t0 = (t.at.sp.page0 + t.at.tile * kTilePages) * kBlock;
+        m.lo = t.at.sp.lo;
+        m.n = t.at.sp.n;
+        m.flags = (t.id >= 0 ? OK0 : 0) | (id1 >= 0 ? OK1 : 0) | (first ? FIRST : 0) | (last ? LAST : 0) |
+                  (t.at.seg_first >= wk.begin && t.at.seg_first + t.at.sp.tiles <= wk.end ? WHOLE : 0);
+        m.seg = seg;
+        m.slot = piece_slot(wk, t.at.seg_first);
+        *sh.meta(s) = m;
+        mbar_arrive(kf);
+      }
+      __syncwarp();
+    }
+    unit += 16;
+  }
+  if (ok) {  // the end
+    const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+    ok = __all_sync(0xffffffffu, mbar_wait(sh.bar(EMPTY + s), ph ^ 1, sh.abort_flag()));
+    if (ok && lane == 0) {
+      sh.meta(s)->flags = END;
+      mbar_arrive(sh.bar(K_FULL + s));
+      mbar_arrive(sh.bar(K_FULL + s));
+    }
+  }
+  if (!ok && lane == 0) {
+    give_up(sh);
+    // nothing may land in shared memory after the CTA has gone
+    for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j) {
+      mbar_wait_drain(sh.bar(K_FULL + j % kStages), (j / kStages) & 1, kWaitCycles / 4);
+      mbar_wait_drain(sh.bar(V_FULL + j % kStages), (j / kStages) & 1, kWaitCycles / 4);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ products (warp 5)
 
 // The query heads as two e4m3 terms each: rows g and 8 + g of the K-major operand, and the factors
-// that scores are multiplied by. A head with an infinite number gets a NaN factor. u: dims 4 lane .. 4 lane + 3 of
-// every head, bf16.
+// that scores are multiplied by. A head with an infinite number gets a NaN factor.
 template <int MG>
-__device__ __forceinline__ void write_q(const Kv8AttnArgs& a, const uint2 (&u)[MG], uint8_t* q, float* factor) {
+__device__ __forceinline__ void write_q(const Kv8AttnArgs& a, const Shared& sh, const uint8_t* raw) {
   const int lane = threadIdx.x & 31;
+  uint8_t* q = sh.queries();
 #pragma unroll
   for (int g = 0; g < MG; ++g) {
     if (g >= a.G) break;
-    float x[4] = {__uint_as_float(u[g].x << 16), __uint_as_float(u[g].x & 0xffff0000u), __uint_as_float(u[g].y << 16),
-                  __uint_as_float(u[g].y & 0xffff0000u)};
+    const uint2 u = reinterpret_cast<const uint2*>(raw)[g * 32 + lane];
+    float x[4] = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
+                  __uint_as_float(u.y & 0xffff0000u)};
     const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
     // 2^e with top / 2^e in [128, 256); tiny heads share the smallest e, whose inverse is finite
     const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 7, -120);
@@ -120,113 +250,44 @@ __device__ __forceinline__ void write_q(const Kv8AttnArgs& a, const uint2 (&u)[M
     const int at = (((lane >> 2) ^ (g & 7)) << 4) + (lane & 3) * 4;  // 128-byte swizzle
     *reinterpret_cast<uint32_t*>(q + g * 128 + at) = t1;
     *reinterpret_cast<uint32_t*>(q + (8 + g) * 128 + at) = t2;
-    if (lane == 0) factor[g] = top < CUDART_INF_F ? __uint_as_float((uint32_t)(127 + e) << 23) * a.scale : CUDART_NAN_F;
+    if (lane == 0) sh.factors()[g] = top < CUDART_INF_F ? __uint_as_float((uint32_t)(127 + e) << 23) * a.scale : CUDART_NAN_F;
   }
 }
 
-// A batch is 32 pages: lane i has the id and the scales of page i. The next batch's ids are under
-// way while one is loaded. A segment's queries follow its first tile, up to four segments ahead of the
-// products, so that short sequences do not wait for them.
+// Lane 0 waits and issues; the warp turns a segment's queries into an operand while the softmax of the
+// segment before ends.
 template <int MG>
-__device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtensorMap* mk, const CUtensorMap* mv, const Work& wk) {
-  const int lane = threadIdx.x & 31;
-  Walk k(a, wk);
-  uint32_t it = 0, seg = 0;
-  bool ok = true;
-  for (; ok && k.next(); ++seg) {
-    uint2 q[MG];
-#pragma unroll
-    for (int g = 0; g < MG; ++g)
-      if (g < a.G)
-        q[g] = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)a.q + (((size_t)k.b * a.Hkv + k.h) * a.G + g) * kHd) + lane);
-    const int* table = a.table + (size_t)k.b * a.max_pages;
-    const int page_end = min(k.sp.page0 + k.tile1 * kTilePages, (k.sp.n + kBlock - 1) / kBlock);
-    auto page_id = [&](int p) { return p < page_end ? __ldg(table + p) : -1; };
-    int p0 = k.sp.page0 + k.tile0 * kTilePages;  // first page of the batch
-    int id_next = page_id(p0 + lane);
-    for (int i = k.tile0; ok && i < k.tile1; p0 += 32) {
-      int id = id_next;
-      id_next = page_id(p0 + 32 + lane);
-      float ks = 0.f, vs = 0.f;
-      if ((unsigned)id < (unsigned)a.n_pages) {
-        ks = __ldg(a.ks + (size_t)id * a.Hkv + k.h);
-        vs = __ldg(a.vs + (size_t)id * a.Hkv + k.h);
-      } else {
-        if (p0 + lane < page_end) atomicOr(sh.err(), LR_DEVERR_PAGE);
-        id = -1;
-      }
-      for (int j = 0; j < 32 && i < k.tile1; j += kTilePages, ++i, ++it) {
-        const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(sh.bar(EMPTY + s), ph ^ 1, sh.abort_flag())))) break;
-        const int id0 = __shfl_sync(0xffffffffu, id, j), id1 = __shfl_sync(0xffffffffu, id, j + 1);
-        if (lane == 0) {
-          const uint32_t bytes = ((id0 >= 0) + (id1 >= 0)) * kPageBytes;
-          mbar_arrive_expect_tx(sh.bar(K_FULL + s), bytes);
-          if (id0 >= 0) tma_load_3d(sh.keys(s), mk, sh.bar(K_FULL + s), 0, k.h * kBlock, id0);
-          if (id1 >= 0) tma_load_3d(sh.keys(s) + kPageBytes, mk, sh.bar(K_FULL + s), 0, k.h * kBlock, id1);
-          mbar_arrive_expect_tx(sh.bar(V_FULL + s), bytes);
-          if (id0 >= 0) tma_load_3d(sh.values(s), mv, sh.bar(V_FULL + s), 0, k.h * kBlock, id0);
-          if (id1 >= 0) tma_load_3d(sh.values(s) + kPageBytes, mv, sh.bar(V_FULL + s), 0, k.h * kBlock, id1);
-        }
-        Meta m;
-        m.ks[0] = __shfl_sync(0xffffffffu, ks, j);
-        m.ks[1] = __shfl_sync(0xffffffffu, ks, j + 1);
-        m.vs[0] = __shfl_sync(0xffffffffu, vs, j);
-        m.vs[1] = __shfl_sync(0xffffffffu, vs, j + 1);
-        if (lane == 0) {
-          m.ok[0] = id0 >= 0;
-          m.ok[1] = id1 >= 0;
-          *sh.meta(s) = m;
-          mbar_arrive(sh.bar(K_FULL + s));
-        }
-        if (i == k.tile0) {
-          const uint32_t buf = seg % kQBufs;
-          if (!(ok = __all_sync(0xffffffffu, mbar_wait(sh.bar(Q_FREE + buf), ((seg / kQBufs) & 1) ^ 1, sh.abort_flag())))) {
-            ++it;  // its loads are under way
-            break;
-          }
-          write_q<MG>(a, q, sh.queries(buf), sh.factors(buf));
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(sh.bar(Q_READY + buf));
-        }
-      }
-    }
-  }
-  if (!ok && lane == 0) {
-    give_up(sh);
-    // nothing may land in shared memory after the CTA has gone
-    for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j) {
-      mbar_wait_drain(sh.bar(K_FULL + j % kStages), (j / kStages) & 1, kWaitCycles / 4);
-      mbar_wait_drain(sh.bar(V_FULL + j % kStages), (j / kStages) & 1, kWaitCycles / 4);
-    }
-  }
-}
-
-// ------------------------------------------------------------------ products (one thread of warp 5)
-template <int MG>
-__device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, uint32_t tmem) {
+__device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
   constexpr int NP = MG <= 4 ? 16 : 32;
   const uint32_t id_s = idesc_e4m3_f32(128, 16, false, false), id_o = idesc_e4m3_f32(128, NP, true, true);
-  const uint32_t p = smem_u32(sh.base + Layout::kOffP);
-  Walk k(a, wk);
-  uint32_t it = 0, seg = 0;
+  const uint32_t q = smem_u32(sh.queries()), p = smem_u32(sh.base + Layout::kOffP);
+  const int lane = threadIdx.x & 31;
   bool ok = true;
-  for (; ok && k.next(); ++seg) {
-    const uint32_t buf = seg % kQBufs, q = smem_u32(sh.queries(buf));
-    ok = mbar_wait(sh.bar(Q_READY + buf), (seg / kQBufs) & 1, sh.abort_flag());
-    for (int i = k.tile0; ok && i < k.tile1; ++i, ++it) {
-      const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-      if (!(ok = mbar_wait(sh.bar(K_FULL + s), ph, sh.abort_flag()))) break;
+  for (uint32_t it = 0;; ++it) {
+    const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+    if (!(ok = __all_sync(0xffffffffu, mbar_wait(sh.bar(K_FULL + s), ph, sh.abort_flag())))) break;
+    const int flags = sh.meta(s)->flags;
+    if (flags & END) break;
+    if (flags & FIRST) {  // the scores of the last segment have been read: nothing uses its queries any more
+      write_q<MG>(a, sh, sh.raw_queries(s));
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(sh.bar(Q_READY));
+    }
+    if (lane == 0) {
       tc_fence_after();
-      const uint32_t kb = smem_u32(sh.keys(s)), vb = smem_u32(sh.values(s));
+      const uint32_t kb = smem_u32(sh.keys(s));
 #pragma unroll
       for (int x = 0; x < kHd / 32; ++x)
         mma_e4m3(tmem + kColS, sw128_desc(kb + x * 32, 16, 1024), sw128_desc(q + x * 32, 16, 1024), id_s, x != 0);
       mma_commit(sh.bar(S_FULL));
-      if (!(ok = mbar_wait(sh.bar(V_FULL + s), ph, sh.abort_flag()))) break;
-      if (!(ok = mbar_wait(sh.bar(P_READY), it & 1, sh.abort_flag()))) break;
+    }
+    __syncwarp();
+    ok = mbar_wait(sh.bar(V_FULL + s), ph, sh.abort_flag()) && mbar_wait(sh.bar(P_READY), it & 1, sh.abort_flag());
+    if (!(ok = __all_sync(0xffffffffu, ok))) break;
+    if (lane == 0) {
       tc_fence_after();
+      const uint32_t vb = smem_u32(sh.values(s));
 #pragma unroll
       for (int x = 0; x < kTileTokens / 32; ++x)  // two of K = 32 for each page
         mma_e4m3(tmem + kColO + (x >> 1) * NP, sw128_desc(vb + x * 4096, 0, 1024), plain_mn_desc(p + x * 512, 128, 2048), id_o,
@@ -234,46 +295,54 @@ __device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, const Wor
       mma_commit(sh.bar(O_FULL));
       mma_commit(sh.bar(EMPTY + s));
     }
+    __syncwarp();
   }
-  if (!ok) give_up(sh);
-  mma_commit(sh.bar(DRAIN));  // every product has completed before shared memory and TMEM go
-  mbar_wait_drain(sh.bar(DRAIN), 0, kWaitCycles / 4);
+  if (lane == 0) {
+    if (!ok) give_up(sh);
+    mma_commit(sh.bar(DRAIN));  // every product has completed before shared memory and TMEM go
+    mbar_wait_drain(sh.bar(DRAIN), 0, kWaitCycles / 4);
+  }
 }
 
 // ------------------------------------------------------------------ softmax and sums (warps 0-3)
 
 template <int MG>
-__device__ void attend(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, uint32_t tmem) {
+__device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
   constexpr int NP = MG <= 4 ? 16 : 32;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const uint32_t tm = tmem + ((uint32_t)(warp * 32) << 16);
   float* wmax = reinterpret_cast<float*>(sh.base + Layout::kOffMax);
+  float* red = reinterpret_cast<float*>(sh.base + Layout::kOffRed);
   const int G = a.G;
-  Walk k(a, wk);
-  uint32_t it = 0, seg = 0;
-  bool ok = true;  // once a wait has failed the rest runs through without waiting: nobody is left at a barrier
+  uint32_t seg = 0;
+  bool ok = true;
   auto wait = [&](int bar, uint32_t parity) {
     if (ok && !(ok = mbar_wait(sh.bar(bar), parity, sh.abort_flag()))) give_up(sh);
   };
-  for (; k.next(); ++seg) {
-    const size_t row0 = ((size_t)k.b * a.Hkv + k.h) * G;
-    const uint32_t buf = seg % kQBufs;
-    wait(Q_READY + buf, (seg / kQBufs) & 1);
-    float qs[MG], m[MG], l[MG], acc[MG];
-#pragma unroll
-    for (int g = 0; g < MG; ++g) {
-      qs[g] = g < G ? sh.factors(buf)[g] : 0.f;
-      m[g] = -CUDART_INF_F;
-      l[g] = acc[g] = 0.f;
+  float qs[MG], m[MG], l[MG], acc[MG];
+  for (uint32_t it = 0;; ++it) {
+    const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+    wait(K_FULL + s, ph);
+    Meta meta = *sh.meta(s);
+    if (!ok) meta.flags = 0;
+    if (meta.flags & END) {
+      soft_all(ok);
+      break;
     }
-    for (int i = k.tile0; i < k.tile1; ++i, ++it) {
-      const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-      const int t0 = (k.sp.page0 + i * kTilePages) * kBlock, t = t0 + tid, half = warp >> 1;
-      wait(K_FULL + s, ph);
-      const Meta* meta = sh.meta(s);
-      const float ks = meta->ks[half], vs0 = meta->vs[0], vs1 = meta->vs[1];
-      const bool both = meta->ok[0] & meta->ok[1];
-      const bool seen = t >= k.sp.lo && t < k.sp.n && meta->ok[half];
+    if (meta.flags & FIRST) {
+      wait(Q_READY, seg++ & 1);
+#pragma unroll
+      for (int g = 0; g < MG; ++g) {
+        qs[g] = g < G ? sh.factors()[g] : 0.f;
+        m[g] = -CUDART_INF_F;
+        l[g] = acc[g] = 0.f;
+      }
+    }
+    {
+      const int t = meta.t0 + tid, half = warp >> 1;
+      const float ks = half ? meta.ks[1] : meta.ks[0], vs0 = meta.vs[0], vs1 = meta.vs[1];
+      const bool both = (meta.flags & (OK0 | OK1)) == (OK0 | OK1);
+      const bool seen = t >= meta.lo && t < meta.n && (meta.flags & (OK0 << half));
       wait(S_FULL, it & 1);
       tc_fence_after();
       float x[MG];
@@ -293,7 +362,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, u
         const float top = warp_max(x[g]);
         if (lane == g) wm[warp * 8 + g] = top;
       }
-      soft_sync();
+      if (!soft_all(ok)) break;  // after a failed wait all leave together: nobody is left at a barrier
       float old[MG], now[MG], p[MG];
 #pragma unroll
       for (int g = 0; g < MG; ++g) {
@@ -331,7 +400,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, u
                              term[1][0] | (term[1][1] << 16), term[1][2] | (term[1][3] << 16));
         prow[kTileTokens] = make_uint4(term[2][0] | (term[2][1] << 16), term[2][2] | (term[2][3] << 16), 0u, 0u);
       }
-      if (t0 < k.sp.lo || t0 + kTileTokens > k.sp.n || !both) {
+      if (meta.t0 < meta.lo || meta.t0 + kTileTokens > meta.n || !both) {
         // value rows outside the attended tokens may hold anything, NaN codes among it
         wait(V_FULL + s, ph);
         if (!seen) {
@@ -376,10 +445,9 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, u
         }
       }
     }
+    if (!(meta.flags & LAST)) continue;
     // the sums of p are spread over the threads
-    float* red = wmax;
-    soft_sync();
-    if (tid == 0) mbar_arrive(sh.bar(Q_FREE + buf));
+    const size_t row0 = (size_t)meta.seg * G;
 #pragma unroll
     for (int g = 0; g < MG; ++g) {
       const float v = warp_sum(l[g]);
@@ -389,8 +457,8 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, const Work& wk, u
 #pragma unroll
     for (int g = 0; g < MG; ++g) l[g] = (red[g] + red[8 + g]) + (red[16 + g] + red[24 + g]);
 
-    if (!k.whole()) {
-      float* slot = a.part + (size_t)piece_slot(k) * a.part_stride;
+    if (!(meta.flags & WHOLE)) {
+      float* slot = a.part + (size_t)meta.slot * a.part_stride;
 #pragma unroll
       for (int g = 0; g < MG; ++g) {
         if (g >= G) break;
@@ -433,10 +501,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       mbar_init(sh.bar(V_FULL + i), 1);
       mbar_init(sh.bar(EMPTY + i), 1);
     }
-    for (int i = 0; i < kQBufs; ++i) {
-      mbar_init(sh.bar(Q_READY + i), 1);
-      mbar_init(sh.bar(Q_FREE + i), 1);
-    }
+    mbar_init(sh.bar(Q_READY), 1);
     mbar_init(sh.bar(S_FULL), 1);
     mbar_init(sh.bar(P_READY), kSoft / 32);
     mbar_init(sh.bar(O_FULL), 1);
@@ -454,7 +519,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     tmem_relinquish();
   }
   // rows of absent query heads stay zero
-  for (int i = threadIdx.x; i < kQBufs * 2048 / 16; i += kThreads)
+  for (int i = threadIdx.x; i < 2048 / 16; i += kThreads)
     reinterpret_cast<uint4*>(smem + Layout::kOffQ)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async_smem();
   tc_fence_before();
@@ -463,11 +528,11 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   if (warp < 4) {
-    attend<MG>(a, sh, wk, tmem);
+    attend<MG>(a, sh, tmem);
   } else if (warp == 4) {
-    load_tiles<MG>(a, sh, &mk, &mv, wk);
-  } else if (lane == 0) {
-    issue_products<MG>(a, sh, wk, tmem);
+    load_tiles(a, sh, &mk, &mv, wk);
+  } else {
+    issue_products<MG>(a, sh, tmem);
   }
   __syncwarp();
   tc_fence_before();

@@ -4,6 +4,7 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <limits.h>
 #include <math_constants.h>
 
 #include "lr_common.cuh"
@@ -51,9 +52,10 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
 
 // ------------------------------------------------------------------ attention: the division of work
 //
-// A segment is one (sequence, KV head); its tokens are cut into tiles of two pages. The tiles
-// of all segments, in the order of (sequence, head, page), are divided evenly among the CTAs: CTA c
-// takes tiles [c W / C, (c + 1) W / C), so ragged lengths cost nothing and one long sequence
+// A segment is one (sequence, KV head); its tokens are cut into tiles of two pages. The segments, in
+// the order of (sequence, head), are laid out on a line of units, one for each tile and kSegmentUnits at
+// the end for what a segment costs by itself, and the line is divided evenly among the CTAs: CTA c
+// takes units [c W / C, (c + 1) W / C), so ragged lengths cost nothing and one long sequence
 // fills the machine. A CTA's range touches at most two segments that others share: its first
 // and its last one. What it has of those are pieces (unnormalised sums with their maximum) in the
 // slots 2c and 2c + 1; a second kernel joins a segment's pieces in the order of the CTAs. (Joined by the
@@ -62,11 +64,13 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
 
 constexpr int kTilePages = 2;
 constexpr int kTileTokens = kTilePages * kBlock;
+constexpr int kSegmentUnits = 1;
 
 struct Span {
   int lo, n;        // tokens [lo, n) are attended
   int page0;        // page (index in the sequence) of the first tile
   int tiles;        // tiles of one head
+  int units;        // its stretch of the line
 };
 
 __device__ __forceinline__ Span seq_span(const Kv8AttnArgs& a, int b) {
@@ -74,18 +78,18 @@ __device__ __forceinline__ Span seq_span(const Kv8AttnArgs& a, int b) {
   s.n = min(max(__ldg(a.lens + b), 0), a.max_pages * kBlock);
   s.lo = a.window > 0 ? max(0, s.n - a.window) : 0;
   s.page0 = s.lo / kBlock;
-  s.tiles = ((s.n + kBlock - 1) / kBlock - s.page0 + kTilePages - 1) / kTilePages;
-  if (s.n == 0) s.tiles = 0;
+  s.tiles = s.n == 0 ? 0 : ((s.n + kBlock - 1) / kBlock - s.page0 + kTilePages - 1) / kTilePages;
+  s.units = s.n == 0 ? 0 : s.tiles + kSegmentUnits;
   return s;
 }
 
-// A CTA's range of tiles and where it starts.
+// A CTA's range of units and where it starts.
 struct Work {
-  long long begin, end;  // tiles of the whole batch
-  long long total;
-  int active;            // CTAs that have work
-  int b;                 // sequence of the first tile
-  long long b_first;     // first tile of that sequence
+  long long begin, end;
+  long long total;       // of the whole batch
+  int active;            // CTAs that have a range
+  int b;                 // sequence of the first unit
+  long long b_first;     // first unit of that sequence
 };
 
 // Called by all NT threads of the CTA; `scratch` holds NT + 4 long longs of shared memory.
@@ -94,7 +98,7 @@ __device__ __forceinline__ Work find_work(const Kv8AttnArgs& a, long long* scrat
   const int tid = threadIdx.x;
   const int per = (a.B + NT - 1) / NT, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += (long long)seq_span(a, b).tiles * a.Hkv;
+  for (int b = b0; b < b1; ++b) mine += (long long)seq_span(a, b).units * a.Hkv;
   // inclusive scan over the warp, then over the warps
   long long run = mine;
   const int lane = tid & 31, warp = tid >> 5;
@@ -122,7 +126,7 @@ __device__ __forceinline__ Work find_work(const Kv8AttnArgs& a, long long* scrat
   if (has && wk.begin >= first && wk.begin < first + mine) {
     long long at = first;
     for (int b = b0; b < b1; ++b) {
-      const long long n = (long long)seq_span(a, b).tiles * a.Hkv;
+      const long long n = (long long)seq_span(a, b).units * a.Hkv;
       if (wk.begin < at + n) {
         scratch[NT] = b;
         scratch[NT + 1] = at;
@@ -137,40 +141,56 @@ __device__ __forceinline__ Work find_work(const Kv8AttnArgs& a, long long* scrat
   return wk;
 }
 
-// The CTA whose range holds tile t, for total tiles over `active` CTAs: largest c with
+// The CTA whose range holds unit t, for total units over `active` CTAs: largest c with
 // c * total / active <= t.
-__device__ __forceinline__ int cta_of_tile(long long t, long long total, int active) {
+__device__ __forceinline__ int cta_of_unit(long long t, long long total, int active) {
   return (int)(((t + 1) * active - 1) / total);
 }
 
-// Walks the segments of a CTA's range in order.
-struct Walk {
-  const Kv8AttnArgs& a;
-  Work wk;
-  long long at;       // next tile of the batch
+// A place on the line that moves forward.
+struct Place {
   int b, h;
   Span sp;
-  long long b_first;
-  // the current segment's part in this range
-  int tile0, tile1;   // tiles of the segment, relative to its start
-  long long seg_first;
+  long long b_first, seg_first;  // first unit of the sequence, of the segment
+  int tile;                      // >= sp.tiles in a segment's last units
 
-  __device__ Walk(const Kv8AttnArgs& a_, const Work& w) : a(a_), wk(w), at(w.begin), b(w.b), b_first(w.b_first) {
-    if (at < wk.end) sp = seq_span(a, b);
+  __device__ __forceinline__ void start(const Kv8AttnArgs& a, const Work& wk) {
+    b = wk.b;
+    b_first = wk.b_first;
+    sp = seq_span(a, b);
+  }
+  __device__ __forceinline__ void seek(const Kv8AttnArgs& a, long long unit) {
+    while (unit >= b_first + (long long)sp.units * a.Hkv) {
+      b_first += (long long)sp.units * a.Hkv;
+      sp = seq_span(a, ++b);
+    }
+    const long long in = unit - b_first;
+    h = in <= INT_MAX ? (int)in / sp.units : (int)(in / sp.units);
+    seg_first = b_first + (long long)h * sp.units;
+    tile = (int)(unit - seg_first);
+  }
+};
+
+// Walks the segments of a CTA's range in order.
+struct Walk : Place {
+  const Kv8AttnArgs& a;
+  Work wk;
+  long long at;       // next unit
+  int tile0, tile1;   // the range's tiles of the current segment
+
+  __device__ Walk(const Kv8AttnArgs& a_, const Work& w) : a(a_), wk(w), at(w.begin) {
+    if (at < wk.end) start(a, wk);
   }
   // Moves to the next segment with tiles in the range; false at its end.
   __device__ bool next() {
-    if (at >= wk.end) return false;
-    while (at >= b_first + (long long)sp.tiles * a.Hkv) {
-      b_first += (long long)sp.tiles * a.Hkv;
-      sp = seq_span(a, ++b);
+    while (at < wk.end) {
+      seek(a, at);
+      at = seg_first + sp.units;
+      tile0 = tile;
+      tile1 = (int)min((long long)sp.tiles, wk.end - seg_first);
+      if (tile0 < tile1) return true;
     }
-    h = (int)((at - b_first) / sp.tiles);
-    seg_first = b_first + (long long)h * sp.tiles;
-    tile0 = (int)(at - seg_first);
-    tile1 = (int)min((long long)sp.tiles, wk.end - seg_first);
-    at = seg_first + tile1;
-    return true;
+    return false;
   }
   __device__ bool whole() const { return tile0 == 0 && tile1 == sp.tiles; }
 };
@@ -209,9 +229,9 @@ __device__ __forceinline__ T joined_value(const Kv8AttnArgs& a, size_t row, int 
 
 // ---- pieces of a split segment
 
-// The slot of this CTA's piece of the walk's segment.
-__device__ __forceinline__ int piece_slot(const Walk& k) {
-  return 2 * blockIdx.x + (k.wk.begin < k.seg_first ? 1 : 0);
+// The slot of this CTA's piece of a segment.
+__device__ __forceinline__ int piece_slot(const Work& wk, long long seg_first) {
+  return 2 * blockIdx.x + (wk.begin < seg_first ? 1 : 0);
 }
 
 // The CTAs that share a segment, and the slot of each one's piece.
@@ -224,8 +244,8 @@ __device__ __forceinline__ Pieces pieces_of(const Walk& k) {
   Pieces p;
   const long long total = k.wk.total;
   const int active = k.wk.active;
-  p.c0 = cta_of_tile(k.seg_first, total, active);
-  p.n = cta_of_tile(k.seg_first + k.sp.tiles - 1, total, active) - p.c0 + 1;
+  p.c0 = cta_of_unit(k.seg_first, total, active);
+  p.n = cta_of_unit(k.seg_first + k.sp.tiles - 1, total, active) - p.c0 + 1;
   p.mid = total * p.c0 / active < k.seg_first;
   return p;
 }

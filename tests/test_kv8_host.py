@@ -104,10 +104,11 @@ def test_null_cache_and_lse(lib):
 
 
 def _divide(tiles, n_cta):
-    """The attention's division of the segments' tiles, as its kernels do it: (segment, first, last + 1)
-    pieces of every CTA, and the pieces' slots."""
-    total, active = sum(tiles), min(n_cta, sum(tiles))
-    first = [sum(tiles[:i]) for i in range(len(tiles))]
+    """The attention's division of the segments' tiles, as its kernels do it (a segment takes one unit more than
+    it has tiles): (CTA, first, last + 1) pieces of every segment, and the pieces' slots."""
+    units = [t + 1 if t else 0 for t in tiles]
+    total, active = sum(units), min(n_cta, sum(units))
+    first = [sum(units[:i]) for i in range(len(tiles))]
     pieces = {i: [] for i in range(len(tiles))}
     slots = {}
     for c in range(active):
@@ -115,6 +116,9 @@ def _divide(tiles, n_cta):
         while at < end:
             s = max(i for i in range(len(tiles)) if tiles[i] and first[i] <= at)
             stop = min(first[s] + tiles[s], end)
+            if stop <= at:  # only the unit behind the tiles
+                at = first[s] + units[s]
+                continue
             whole = at == first[s] and stop == first[s] + tiles[s]
             pieces[s].append((c, at, stop))
             if not whole:
@@ -125,7 +129,7 @@ def _divide(tiles, n_cta):
                 slots[(c, s)] = slot
                 assert c0 <= c <= c1
                 pieces.setdefault(("span", s), (c0, c1))
-            at = stop
+            at = first[s] + units[s]
     return first, pieces, slots
 
 
