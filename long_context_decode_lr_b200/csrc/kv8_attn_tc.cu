@@ -35,7 +35,7 @@ constexpr int kThreads = 192, kSoft = 128;
 constexpr int kStages = 3;
 constexpr int kPageBytes = kBlock * kHd;
 constexpr int kTileBytes = kTilePages * kPageBytes;  // of K, and of V
-constexpr int kTmemCols = 128, kColS = 0, kColO = 32;
+constexpr int kColS = 0, kColO = 32;  // TMEM: two S of 16 columns, two O' of 2 NP
 
 // What the loading warp says of the tile in a stage.
 enum Flag { OK0 = 1, OK1 = 2, FIRST = 4, LAST = 8, WHOLE = 16, END = 32 };
@@ -43,29 +43,29 @@ struct __align__(16) Meta {
   float ks[2], vs[2];    // scales of its two pages
   int t0, lo, n, flags;  // its first token, the attended ones; which pages there are (OK0, OK1), first or last
                          // tile of the segment here, all of the segment here, no tile: the end
-  int seg, slot;         // b * Hkv + h, and where a piece of it goes
+  int head, slot;        // b * Hkv + h, and where a piece of it goes
   int pad[2];
 };
 
 struct Layout {
   static constexpr int kOffRing = 0;                         // stages of K, V
-  static constexpr int kOffQ = kStages * 2 * kTileBytes;     // 16 rows of 128 bytes
-  static constexpr int kOffP = kOffQ + 2048;                 // [2][128 tokens][16 bytes]
-  static constexpr int kOffRawQ = kOffP + 4096;              // [kStages][8][128] bf16
-  static constexpr int kOffMeta = kOffRawQ + kStages * 2048;
+  static constexpr int kOffQ = kStages * 2 * kTileBytes;     // [kStages][16 rows of 128 bytes]
+  static constexpr int kOffP = kOffQ + kStages * 2048;             // [2][2][128 tokens][16 bytes]
+  static constexpr int kOffMeta = kOffP + 2 * 4096;
   static constexpr int kOffMax = kOffMeta + kStages * (int)sizeof(Meta);  // [2][4 warps][8]
   static constexpr int kOffRed = kOffMax + 2 * 4 * 8 * 4;    // [4 warps][8]
-  static constexpr int kOffQs = kOffRed + 4 * 8 * 4;         // [8]
-  static constexpr int kOffBar = kOffQs + 32;
-  static constexpr int kOffMisc = kOffBar + 128;
-  static constexpr int kOffScratch = kOffMisc + 16;                       // find_work
-  static constexpr int kBytes = kOffScratch + (kThreads + 4) * 8;
+  static constexpr int kOffQs = kOffRed + 4 * 8 * 4;         // [2][8]
+  static constexpr int kOffBar = kOffQs + 64;
+  static constexpr int kOffMisc = kOffBar + 160;
+  static constexpr int kOffScratch = kOffP;                  // of find_work, before there are any weights
+  static constexpr int kBytes = kOffMisc + 16;
 };
-static_assert(Layout::kOffMeta % 16 == 0 && Layout::kOffBar % 8 == 0 && Layout::kOffScratch % 8 == 0, "alignment");
+static_assert(Layout::kOffMeta % 16 == 0 && Layout::kOffBar % 8 == 0, "alignment");
+static_assert((kThreads + 4) * 8 <= 2 * 4096, "scratch");
 static_assert(2 * (Layout::kBytes + 1024) <= 227 * 1024, "two CTAs per SM");
 
-enum Bar { K_FULL = 0, V_FULL = K_FULL + kStages, EMPTY = V_FULL + kStages, Q_READY = EMPTY + kStages, S_FULL, P_READY, O_FULL, DRAIN, kBars };
-static_assert(kBars * 8 <= 128, "barriers");
+enum Bar { K_FULL = 0, V_FULL = K_FULL + kStages, EMPTY = V_FULL + kStages, Q_READY = EMPTY + kStages, S_FULL = Q_READY + 2, P_READY = S_FULL + 2, O_FULL = P_READY + 2, DRAIN = O_FULL + 2, kBars };
+static_assert(kBars * 8 <= 160, "barriers");
 
 // Barriers of the softmax warps; soft_all also says whether `ok` held in all of them.
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
@@ -96,15 +96,18 @@ __device__ __forceinline__ uint64_t plain_mn_desc(uint32_t saddr, uint32_t k_byt
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(k_bytes >> 4) << 16) | ((uint64_t)(n_bytes >> 4) << 32) | (1ull << 46);
 }
 
+template <int MG>
+__host__ __device__ constexpr int tmem_cols() { return MG <= 4 ? 128 : 256; }
+
 struct Shared {
   uint8_t* base;
   __device__ uint64_t* bar(int i) const { return reinterpret_cast<uint64_t*>(base + Layout::kOffBar) + i; }
   __device__ volatile int* abort_flag() const { return reinterpret_cast<volatile int*>(base + Layout::kOffMisc + 4); }
   __device__ int* err() const { return reinterpret_cast<int*>(base + Layout::kOffMisc + 8); }
   __device__ Meta* meta(int s) const { return reinterpret_cast<Meta*>(base + Layout::kOffMeta) + s; }
-  __device__ uint8_t* queries() const { return base + Layout::kOffQ; }
-  __device__ uint8_t* raw_queries(int s) const { return base + Layout::kOffRawQ + s * 2048; }
-  __device__ float* factors() const { return reinterpret_cast<float*>(base + Layout::kOffQs); }
+  __device__ uint8_t* queries(int i) const { return base + Layout::kOffQ + i * 2048; }
+  __device__ uint8_t* weights(int i) const { return base + Layout::kOffP + i * 4096; }
+  __device__ float* factors(int i) const { return reinterpret_cast<float*>(base + Layout::kOffQs) + i * 8; }
   __device__ uint8_t* keys(int s) const { return base + Layout::kOffRing + s * 2 * kTileBytes; }
   __device__ uint8_t* values(int s) const { return keys(s) + kTileBytes; }
 };
@@ -151,7 +154,7 @@ __device__ __forceinline__ void batch_scales(const Kv8AttnArgs& a, const Shared&
 
 __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtensorMap* mk, const CUtensorMap* mv, const Work& wk) {
   const int lane = threadIdx.x & 31;
-  uint32_t it = 0;
+  uint32_t it = 0, seg = 0;
   bool ok = true;
   Batch next;
   long long unit = wk.begin + (lane >> 1);  // of this lane, in the batch under way
@@ -172,16 +175,18 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
       const uint32_t s = it % kStages, ph = (it / kStages) & 1;
       if (!(ok = __all_sync(0xffffffffu, mbar_wait(sh.bar(EMPTY + s), ph ^ 1, sh.abort_flag())))) break;
       ++it;
+      const bool first = t.at.tile == 0 || unit == wk.begin;
+      seg += __shfl_sync(0xffffffffu, first, src);
       if (lane == src) {
-        const bool first = t.at.tile == 0 || unit == wk.begin;
         const bool last = t.at.tile == t.at.sp.tiles - 1 || unit == wk.end - 1;
-        const int seg = t.at.b * a.Hkv + t.at.h, row = t.at.h * kBlock;
+        const int head = t.at.b * a.Hkv + t.at.h, row = t.at.h * kBlock;
         const uint32_t bytes = ((t.id >= 0) + (id1 >= 0)) * kPageBytes, q_bytes = a.G * kHd * 2;
         uint64_t *kf = sh.bar(K_FULL + s), *vf = sh.bar(V_FULL + s);
         mbar_arrive_expect_tx(kf, bytes + (first ? q_bytes : 0));
         if (t.id >= 0) tma_load_3d(sh.keys(s), mk, kf, 0, row, t.id);
         if (id1 >= 0) tma_load_3d(sh.keys(s) + kPageBytes, mk, kf, 0, row, id1);
-        if (first) bulk_load(sh.raw_queries(s), (const __nv_bfloat16*)a.q + (size_t)seg * a.G * kHd, q_bytes, kf);
+        // the segment three before has no scores to come: the tile that was in this stage is behind its end
+        if (first) bulk_load(sh.queries((seg - 1) % kStages), (const __nv_bfloat16*)a.q + (size_t)head * a.G * kHd, q_bytes, kf);
         mbar_arrive_expect_tx(vf, bytes);
         if (t.id >= 0) tma_load_3d(sh.values(s), mv, vf, 0, row, t.id);
         if (id1 >= 0) tma_load_3d(sh.values(s) + kPageBytes, mv, vf, 0, row, id1);
@@ -195,7 +200,7 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
         m.n = t.at.sp.n;
         m.flags = (t.id >= 0 ? OK0 : 0) | (id1 >= 0 ? OK1 : 0) | (first ? FIRST : 0) | (last ? LAST : 0) |
                   (t.at.seg_first >= wk.begin && t.at.seg_first + t.at.sp.tiles <= wk.end ? WHOLE : 0);
-        m.seg = seg;
+        m.head = head;
         m.slot = piece_slot(wk, t.at.seg_first);
         *sh.meta(s) = m;
         mbar_arrive(kf);
@@ -225,16 +230,21 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
 
 // ------------------------------------------------------------------ products (warp 5)
 
-// The query heads as two e4m3 terms each: rows g and 8 + g of the K-major operand, and the factors
-// that scores are multiplied by. A head with an infinite number gets a NaN factor.
+// The query heads, bf16 rows of 256 bytes at q, become two e4m3 terms each, rows g and 8 + g of the K-major
+// operand in their place, and the factors that scores are multiplied by. A head with an infinite
+// number gets a NaN factor. What is left in the rows of absent heads reaches columns that nobody reads.
 template <int MG>
-__device__ __forceinline__ void write_q(const Kv8AttnArgs& a, const Shared& sh, const uint8_t* raw) {
+__device__ __forceinline__ void write_q(const Kv8AttnArgs& a, uint8_t* q, float* factors) {
   const int lane = threadIdx.x & 31;
-  uint8_t* q = sh.queries();
+  uint2 raw[MG];
+#pragma unroll
+  for (int g = 0; g < MG; ++g)
+    if (g < a.G) raw[g] = reinterpret_cast<const uint2*>(q)[g * 32 + lane];
+  __syncwarp();
 #pragma unroll
   for (int g = 0; g < MG; ++g) {
     if (g >= a.G) break;
-    const uint2 u = reinterpret_cast<const uint2*>(raw)[g * 32 + lane];
+    const uint2 u = raw[g];
     float x[4] = {__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
                   __uint_as_float(u.y & 0xffff0000u)};
     const float top = warp_max(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))));
@@ -250,52 +260,71 @@ __device__ __forceinline__ void write_q(const Kv8AttnArgs& a, const Shared& sh, 
     const int at = (((lane >> 2) ^ (g & 7)) << 4) + (lane & 3) * 4;  // 128-byte swizzle
     *reinterpret_cast<uint32_t*>(q + g * 128 + at) = t1;
     *reinterpret_cast<uint32_t*>(q + (8 + g) * 128 + at) = t2;
-    if (lane == 0) sh.factors()[g] = top < CUDART_INF_F ? __uint_as_float((uint32_t)(127 + e) << 23) * a.scale : CUDART_NAN_F;
+    if (lane == 0) factors[g] = top < CUDART_INF_F ? __uint_as_float((uint32_t)(127 + e) << 23) * a.scale : CUDART_NAN_F;
   }
 }
 
-// Lane 0 waits and issues; the warp turns a segment's queries into an operand while the softmax of the
-// segment before ends.
+// The scores of the next tile go ahead of a tile's value product if its keys are there by the time the product
+// would have to wait for the softmax, so that they are ready when the softmax is. (Polling for whichever is first
+// took issue slots from the softmax: 98 us instead of 91 for 64 sequences of 8 query heads per KV head.)
+// Lane 0 issues; the warp turns a segment's queries into an operand.
 template <int MG>
 __device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
   constexpr int NP = MG <= 4 ? 16 : 32;
   const uint32_t id_s = idesc_e4m3_f32(128, 16, false, false), id_o = idesc_e4m3_f32(128, NP, true, true);
-  const uint32_t q = smem_u32(sh.queries()), p = smem_u32(sh.base + Layout::kOffP);
   const int lane = threadIdx.x & 31;
-  bool ok = true;
-  for (uint32_t it = 0;; ++it) {
-    const uint32_t s = it % kStages, ph = (it / kStages) & 1;
-    if (!(ok = __all_sync(0xffffffffu, mbar_wait(sh.bar(K_FULL + s), ph, sh.abort_flag())))) break;
-    const int flags = sh.meta(s)->flags;
-    if (flags & END) break;
-    if (flags & FIRST) {  // the scores of the last segment have been read: nothing uses its queries any more
-      write_q<MG>(a, sh, sh.raw_queries(s));
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(sh.bar(Q_READY));
-    }
-    if (lane == 0) {
-      tc_fence_after();
-      const uint32_t kb = smem_u32(sh.keys(s));
+  uint32_t qk = 0, pv = 0, seg = 0;  // tiles whose scores and whose value products are issued
+  bool end = false, ok = true;
+  while (!end || pv < qk) {
+    if (!end && qk <= pv + 1) {
+      const uint32_t s = qk % kStages, ph = (qk / kStages) & 1;
+      bool there;
+      if (qk <= pv) there = ok = __all_sync(0xffffffffu, mbar_wait(sh.bar(K_FULL + s), ph, sh.abort_flag()));
+      else there = __all_sync(0xffffffffu, mbar_test(sh.bar(K_FULL + s), ph));
+      if (!ok) break;
+      if (there) {
+        const int flags = sh.meta(s)->flags;
+        if (flags & END) {
+          end = true;
+          continue;
+        }
+        if (flags & FIRST) {  // the factors of the segment before the last have been read
+          write_q<MG>(a, sh.queries(seg % kStages), sh.factors(seg & 1));
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(sh.bar(Q_READY + (seg & 1)));
+          ++seg;
+        }
+        if (lane == 0) {
+          tc_fence_after();
+          const uint32_t kb = smem_u32(sh.keys(s)), q = smem_u32(sh.queries((seg - 1) % kStages));
 #pragma unroll
-      for (int x = 0; x < kHd / 32; ++x)
-        mma_e4m3(tmem + kColS, sw128_desc(kb + x * 32, 16, 1024), sw128_desc(q + x * 32, 16, 1024), id_s, x != 0);
-      mma_commit(sh.bar(S_FULL));
+          for (int x = 0; x < kHd / 32; ++x)
+            mma_e4m3(tmem + kColS + (qk & 1) * 16, sw128_desc(kb + x * 32, 16, 1024), sw128_desc(q + x * 32, 16, 1024), id_s,
+                     x != 0);
+          mma_commit(sh.bar(S_FULL + (qk & 1)));
+        }
+        __syncwarp();
+        ++qk;
+        if (qk <= pv + 1) continue;
+      }
     }
-    __syncwarp();
-    ok = mbar_wait(sh.bar(V_FULL + s), ph, sh.abort_flag()) && mbar_wait(sh.bar(P_READY), it & 1, sh.abort_flag());
+    const uint32_t s = pv % kStages;
+    ok = mbar_wait(sh.bar(P_READY + (pv & 1)), (pv >> 1) & 1, sh.abort_flag()) &&
+         mbar_wait(sh.bar(V_FULL + s), (pv / kStages) & 1, sh.abort_flag());
     if (!(ok = __all_sync(0xffffffffu, ok))) break;
     if (lane == 0) {
       tc_fence_after();
-      const uint32_t vb = smem_u32(sh.values(s));
+      const uint32_t vb = smem_u32(sh.values(s)), p = smem_u32(sh.weights(pv & 1));
 #pragma unroll
       for (int x = 0; x < kTileTokens / 32; ++x)  // two of K = 32 for each page
-        mma_e4m3(tmem + kColO + (x >> 1) * NP, sw128_desc(vb + x * 4096, 0, 1024), plain_mn_desc(p + x * 512, 128, 2048), id_o,
-                 x & 1);
-      mma_commit(sh.bar(O_FULL));
+        mma_e4m3(tmem + kColO + ((pv & 1) * 2 + (x >> 1)) * NP, sw128_desc(vb + x * 4096, 0, 1024),
+                 plain_mn_desc(p + x * 512, 128, 2048), id_o, x & 1);
+      mma_commit(sh.bar(O_FULL + (pv & 1)));
       mma_commit(sh.bar(EMPTY + s));
     }
     __syncwarp();
+    ++pv;
   }
   if (lane == 0) {
     if (!ok) give_up(sh);
@@ -320,6 +349,40 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
     if (ok && !(ok = mbar_wait(sh.bar(bar), parity, sh.abort_flag()))) give_up(sh);
   };
   float qs[MG], m[MG], l[MG], acc[MG];
+  float old[MG], now[MG], vs0, vs1;  // what the tile whose value product is under way is added with
+  auto add_values = [&](uint32_t i) {
+    wait(O_FULL + (i & 1), (i >> 1) & 1);
+    tc_fence_after();
+    if constexpr (MG <= 4) {
+      uint32_t d[32];
+      tmem_ld32(tm + kColO + (i & 1) * 32, d);
+      tmem_ld_wait();
+#pragma unroll
+      for (int g = 0; g < MG; ++g) {
+        float o[2];
+#pragma unroll
+        for (int y = 0; y < 2; ++y)
+          o[y] = fmaf(__uint_as_float(d[16 * y + 8 + g]), 1.f / 1024.f,
+                      fmaf(__uint_as_float(d[16 * y + 4 + g]), 1.f / 32.f, __uint_as_float(d[16 * y + g])));
+        acc[g] = fmaf(acc[g], old[g], fmaf(o[0], vs0, o[1] * vs1) * (now[g] * (1.f / 256.f)));
+      }
+    } else {
+      float o[MG];
+#pragma unroll
+      for (int y = 0; y < 2; ++y) {
+        uint32_t d[32];
+        tmem_ld32(tm + kColO + ((i & 1) * 2 + y) * NP, d);
+        tmem_ld_wait();
+#pragma unroll
+        for (int g = 0; g < MG; ++g) {
+          const float v = fmaf(__uint_as_float(d[16 + g]), 1.f / 1024.f,
+                               fmaf(__uint_as_float(d[8 + g]), 1.f / 32.f, __uint_as_float(d[g])));
+          if (y == 0) o[g] = v * vs0;
+          else acc[g] = fmaf(acc[g], old[g], fmaf(v, vs1, o[g]) * (now[g] * (1.f / 256.f)));
+        }
+      }
+    }
+  };
   for (uint32_t it = 0;; ++it) {
     const uint32_t s = it % kStages, ph = (it / kStages) & 1;
     wait(K_FULL + s, ph);
@@ -330,25 +393,27 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
       break;
     }
     if (meta.flags & FIRST) {
-      wait(Q_READY, seg++ & 1);
+      const int buf = seg & 1;
+      wait(Q_READY + buf, (seg >> 1) & 1);
+      ++seg;
 #pragma unroll
       for (int g = 0; g < MG; ++g) {
-        qs[g] = g < G ? sh.factors()[g] : 0.f;
+        qs[g] = g < G ? sh.factors(buf)[g] : 0.f;
         m[g] = -CUDART_INF_F;
         l[g] = acc[g] = 0.f;
       }
     }
     {
       const int t = meta.t0 + tid, half = warp >> 1;
-      const float ks = half ? meta.ks[1] : meta.ks[0], vs0 = meta.vs[0], vs1 = meta.vs[1];
+      const float ks = half ? meta.ks[1] : meta.ks[0];
       const bool both = (meta.flags & (OK0 | OK1)) == (OK0 | OK1);
       const bool seen = t >= meta.lo && t < meta.n && (meta.flags & (OK0 << half));
-      wait(S_FULL, it & 1);
+      wait(S_FULL + (it & 1), (it >> 1) & 1);
       tc_fence_after();
       float x[MG];
       {
         uint32_t d[16];
-        tmem_ld16(tm + kColS, d);
+        tmem_ld16(tm + kColS + (it & 1) * 16, d);
         tmem_ld_wait();
 #pragma unroll
         for (int g = 0; g < MG; ++g) {
@@ -363,7 +428,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
         if (lane == g) wm[warp * 8 + g] = top;
       }
       if (!soft_all(ok)) break;  // after a failed wait all leave together: nobody is left at a barrier
-      float old[MG], now[MG], p[MG];
+      float p[MG], old_next[MG], now_next[MG];
 #pragma unroll
       for (int g = 0; g < MG; ++g) {
         const float top = fmaxf(fmaxf(wm[g], wm[8 + g]), fmaxf(wm[16 + g], wm[24 + g]));
@@ -371,10 +436,10 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
         p[g] = exp2f(x[g] - (none ? 0.f : top));
         const float mn = fmaxf(m[g], top);
         const float ref = mn == -CUDART_INF_F ? 0.f : mn;
-        old[g] = exp2f(m[g] - ref);
-        now[g] = none ? 0.f : exp2f(top - ref);
+        old_next[g] = exp2f(m[g] - ref);
+        now_next[g] = none ? 0.f : exp2f(top - ref);
         m[g] = mn;
-        l[g] = fmaf(l[g], old[g], p[g] * now[g]);
+        l[g] = fmaf(l[g], old_next[g], p[g] * now_next[g]);
       }
       // the terms of p: two heads to a conversion
       uint32_t term[3][MG / 2];
@@ -391,7 +456,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
           }
         }
       }
-      uint4* prow = reinterpret_cast<uint4*>(sh.base + Layout::kOffP) + tid;
+      uint4* prow = reinterpret_cast<uint4*>(sh.weights(it & 1)) + tid;
       if constexpr (MG <= 4) {
         *prow = make_uint4(term[0][0] | (term[0][1] << 16), term[1][0] | (term[1][1] << 16),
                            term[2][0] | (term[2][1] << 16), 0u);
@@ -412,42 +477,20 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
       fence_proxy_async_smem();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(sh.bar(P_READY));
-      wait(O_FULL, it & 1);
-      tc_fence_after();
-      if constexpr (MG <= 4) {
-        uint32_t d[32];
-        tmem_ld32(tm + kColO, d);
-        tmem_ld_wait();
+      if (lane == 0) mbar_arrive(sh.bar(P_READY + (it & 1)));
+      if (!(meta.flags & FIRST)) add_values(it - 1);
 #pragma unroll
-        for (int g = 0; g < MG; ++g) {
-          float o[2];
-#pragma unroll
-          for (int y = 0; y < 2; ++y)
-            o[y] = fmaf(__uint_as_float(d[16 * y + 8 + g]), 1.f / 1024.f,
-                        fmaf(__uint_as_float(d[16 * y + 4 + g]), 1.f / 32.f, __uint_as_float(d[16 * y + g])));
-          acc[g] = fmaf(acc[g], old[g], fmaf(o[0], vs0, o[1] * vs1) * (now[g] * (1.f / 256.f)));
-        }
-      } else {
-        float o[MG];
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          uint32_t d[32];
-          tmem_ld32(tm + kColO + y * NP, d);
-          tmem_ld_wait();
-#pragma unroll
-          for (int g = 0; g < MG; ++g) {
-            const float v = fmaf(__uint_as_float(d[16 + g]), 1.f / 1024.f,
-                                 fmaf(__uint_as_float(d[8 + g]), 1.f / 32.f, __uint_as_float(d[g])));
-            if (y == 0) o[g] = v * vs0;
-            else acc[g] = fmaf(acc[g], old[g], fmaf(v, vs1, o[g]) * (now[g] * (1.f / 256.f)));
-          }
-        }
+      for (int g = 0; g < MG; ++g) {
+        old[g] = old_next[g];
+        now[g] = now_next[g];
       }
+      vs0 = meta.vs[0];
+      vs1 = meta.vs[1];
     }
     if (!(meta.flags & LAST)) continue;
+    add_values(it);
     // the sums of p are spread over the threads
-    const size_t row0 = (size_t)meta.seg * G;
+    const size_t row0 = (size_t)meta.head * G;
 #pragma unroll
     for (int g = 0; g < MG; ++g) {
       const float v = warp_sum(l[g]);
@@ -501,10 +544,12 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       mbar_init(sh.bar(V_FULL + i), 1);
       mbar_init(sh.bar(EMPTY + i), 1);
     }
-    mbar_init(sh.bar(Q_READY), 1);
-    mbar_init(sh.bar(S_FULL), 1);
-    mbar_init(sh.bar(P_READY), kSoft / 32);
-    mbar_init(sh.bar(O_FULL), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(sh.bar(Q_READY + i), 1);
+      mbar_init(sh.bar(S_FULL + i), 1);
+      mbar_init(sh.bar(P_READY + i), kSoft / 32);
+      mbar_init(sh.bar(O_FULL + i), 1);
+    }
     mbar_init(sh.bar(DRAIN), 1);
     *sh.abort_flag() = 0;
     *sh.err() = 0;
@@ -515,13 +560,9 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     tma_prefetch_desc(&mv);
   }
   if (warp == 5) {
-    tmem_alloc(tmem_holder, kTmemCols);
+    tmem_alloc(tmem_holder, tmem_cols<MG>());
     tmem_relinquish();
   }
-  // rows of absent query heads stay zero
-  for (int i = threadIdx.x; i < 2048 / 16; i += kThreads)
-    reinterpret_cast<uint4*>(smem + Layout::kOffQ)[i] = make_uint4(0u, 0u, 0u, 0u);
-  fence_proxy_async_smem();
   tc_fence_before();
   grid_dependency();
   const Work wk = find_work<kThreads>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
@@ -538,7 +579,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, kTmemCols);
+  if (warp == 5) tmem_dealloc(tmem, tmem_cols<MG>());
   if (threadIdx.x == 0) a.cta_err[blockIdx.x] = *sh.err();
 }
 
