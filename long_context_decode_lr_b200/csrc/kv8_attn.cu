@@ -211,7 +211,7 @@ constexpr int kMaxCtas = 1024;
 template <typename T>
 __global__ void __launch_bounds__(JT) kv8_join_kernel(Kv8AttnArgs a) {
   __shared__ long long scratch[JT + 4];
-  __shared__ float weight[kMaxCtas];
+  __shared__ float weight[kMaxCtas], sum_of[kMaxCtas];
   __shared__ float red[2][JT / 32];
   __shared__ __align__(16) float sums[JT * 4];
   __shared__ int err;
@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(JT) kv8_join_kernel(Kv8AttnArgs a) {
   const Work wk = find_work<JT>(a, scratch);
   Walk k(a, wk);
   // the first of the CTAs whose range starts inside the segment
-  const bool mine = c > 0 && k.next() && k.tile0 > 0 && wk.total * (c - 1) / wk.active <= k.seg_first;
+  const bool mine = c > 0 && k.next() && k.tile0 > 0 && range_begin(wk.total, c - 1, wk.active) <= k.seg_first;
   const bool errors = c == 0 && g == 0;
   if (errors) {
     if (tid == 0) err = 0;
@@ -252,9 +252,23 @@ __global__ void __launch_bounds__(JT) kv8_join_kernel(Kv8AttnArgs a) {
   const Pieces pc = pieces_of(k);
   const size_t row = ((size_t)k.b * a.Hkv + k.h) * a.G + g;
   const int n = pc.n, ml = a.G * hd + g;
+  const int cols = hd / 4, groups = JT / cols, col = tid % cols, group = tid / cols;
+  auto values = [&](int i) {
+    return __ldcg(reinterpret_cast<const float4*>(a.part + (size_t)pc.slot(i) * a.part_stride + g * hd) + col);
+  };
+  // a thread's first pieces are on their way before their weights are known
+  constexpr int kAhead = 10;
+  float4 v[kAhead];
+#pragma unroll
+  for (int x = 0; x < kAhead; ++x) {
+    const int i = group + x * groups;
+    v[x] = group < groups && i < n ? values(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  }
   float m = -CUDART_INF_F;
   for (int i = tid; i < n; i += JT) {
-    const float mi = __ldcg(a.part + (size_t)pc.slot(i) * a.part_stride + ml);
+    const float* at = a.part + (size_t)pc.slot(i) * a.part_stride + ml;
+    const float mi = __ldcg(at);
+    sum_of[i] = __ldcg(at + 8);
     weight[i] = mi;
     m = fmaxf(m, mi);
   }
@@ -267,24 +281,26 @@ __global__ void __launch_bounds__(JT) kv8_join_kernel(Kv8AttnArgs a) {
   for (int i = tid; i < n; i += JT) {
     const float w = exp2f(weight[i] - ref);
     weight[i] = w;
-    l = fmaf(w, __ldcg(a.part + (size_t)pc.slot(i) * a.part_stride + ml + 8), l);
+    l = fmaf(w, sum_of[i], l);
   }
   l = warp_sum(l);
   if (lane == 0) red[1][warp] = l;
   __syncthreads();
   l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  const int cols = hd / 4, groups = JT / cols, col = tid % cols, group = tid / cols;
   if (group < groups) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int i = group; i < n; i += groups) {
+    auto add = [&](int i, const float4& x) {
       const float w = weight[i];
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(a.part + (size_t)pc.slot(i) * a.part_stride + g * hd) + col);
-      s.x = fmaf(w, v.x, s.x);
-      s.y = fmaf(w, v.y, s.y);
-      s.z = fmaf(w, v.z, s.z);
-      s.w = fmaf(w, v.w, s.w);
-    }
+      s.x = fmaf(w, x.x, s.x);
+      s.y = fmaf(w, x.y, s.y);
+      s.z = fmaf(w, x.z, s.z);
+      s.w = fmaf(w, x.w, s.w);
+    };
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x)
+      if (group + x * groups < n) add(group + x * groups, v[x]);
+#pragma unroll 4
+    for (int i = group + kAhead * groups; i < n; i += groups) add(i, values(i));
     reinterpret_cast<float4*>(sums)[group * cols + col] = s;
   }
   const Joined j = join_prev(a, row, m, l);
@@ -317,7 +333,7 @@ cudaError_t launch_attn(const Kv8AttnArgs& a, const Kv8AttnPlan& plan, cudaStrea
 Kv8AttnPlan plan_kv8_attn(const lr_kv8_pages& kv, int n_q_heads, int sm_count) {
   Kv8AttnPlan p{};
   const int G = n_q_heads / kv.n_kv_heads;
-  const long long most = (long long)kv.batch * kv.n_kv_heads * ((kv.max_pages + 1) / 2);  // tiles
+  const long long most = (long long)kv.batch * kv.n_kv_heads * ((kv.max_pages + 1) / 2 + kv8::kSegmentUnits);  // units
   p.tensor = kv.dtype == LR_BF16 && kv.head_dim == 128;
   p.n_cta = (int)std::max(1LL, std::min<long long>(most, std::min(2 * sm_count, kv8::kMaxCtas)));
   p.part_stride = G * kv.head_dim + 16;

@@ -7,8 +7,8 @@
 // before leave over:
 //   q = 2^e (q1 + q2 / 32)              exact for a bf16 number down to 2^-15 of the head's largest
 //                                       (below that off by 2^-22 of it at most);
-//   p = (p1 + p2 / 32 + p3 / 1024) / 256, relative error 2^-14 at most for p >= 2^-14, 2^-28 absolute
-//                                       below, p relative to the largest of the tile.
+//   p = (p1 + p2 / 32 + p3 / 1024) / 256, p rounded to fp16 first: 2^-12 relative at most, 2^-28 absolute
+//                                       for p under 2^-16, p relative to the largest of the tile.
 // Every term is a column of its own, so a tile's products are
 //   S  [128 tokens x 16]     = K q1 | K q2             (M 128, N 16, K 128)
 //   O' [128 dims x 3 heads]  = V^T p1 | V^T p2 | V^T p3 (M 128, N 16 or 32, K 64) for each of the two pages,
@@ -31,7 +31,9 @@ namespace {
 using namespace sm100;
 
 constexpr int kHd = 128;
-constexpr int kThreads = 192, kSoft = 128;
+constexpr int kSoft = 128;  // threads of a softmax group, which has up to four query heads
+constexpr int kHeads = 4;
+constexpr int threads_of(int groups) { return groups * kSoft + 64; }
 constexpr int kStages = 3;
 constexpr int kPageBytes = kBlock * kHd;
 constexpr int kTileBytes = kTilePages * kPageBytes;  // of K, and of V
@@ -52,8 +54,8 @@ struct Layout {
   static constexpr int kOffQ = kStages * 2 * kTileBytes;     // [kStages][16 rows of 128 bytes]
   static constexpr int kOffP = kOffQ + kStages * 2048;             // [2][2][128 tokens][16 bytes]
   static constexpr int kOffMeta = kOffP + 2 * 4096;
-  static constexpr int kOffMax = kOffMeta + kStages * (int)sizeof(Meta);  // [2][4 warps][8]
-  static constexpr int kOffRed = kOffMax + 2 * 4 * 8 * 4;    // [4 warps][8]
+  static constexpr int kOffMax = kOffMeta + kStages * (int)sizeof(Meta);  // [2 groups][2][4 warps][4]
+  static constexpr int kOffRed = kOffMax + 2 * 4 * 8 * 4;    // [2 groups][4 warps][4]
   static constexpr int kOffQs = kOffRed + 4 * 8 * 4;         // [2][8]
   static constexpr int kOffBar = kOffQs + 64;
   static constexpr int kOffMisc = kOffBar + 160;
@@ -61,23 +63,25 @@ struct Layout {
   static constexpr int kBytes = kOffMisc + 16;
 };
 static_assert(Layout::kOffMeta % 16 == 0 && Layout::kOffBar % 8 == 0, "alignment");
-static_assert((kThreads + 4) * 8 <= 2 * 4096, "scratch");
+static_assert((threads_of(2) + 4) * 8 <= 2 * 4096, "scratch");
 static_assert(2 * (Layout::kBytes + 1024) <= 227 * 1024, "two CTAs per SM");
 
 enum Bar { K_FULL = 0, V_FULL = K_FULL + kStages, EMPTY = V_FULL + kStages, Q_READY = EMPTY + kStages, S_FULL = Q_READY + 2, P_READY = S_FULL + 2, O_FULL = P_READY + 2, DRAIN = O_FULL + 2, kBars };
 static_assert(kBars * 8 <= 160, "barriers");
 
-// Barriers of the softmax warps; soft_all also says whether `ok` held in all of them.
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, %0;" ::"n"(kSoft) : "memory"); }
-__device__ __forceinline__ bool soft_all(bool ok) {
+// Barriers of a softmax group; soft_all also says whether `ok` held in all of its threads.
+__device__ __forceinline__ void soft_sync(int group) {
+  asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kSoft) : "memory");
+}
+__device__ __forceinline__ bool soft_all(int group, bool ok) {
   uint32_t r;
   asm volatile(
       "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.u32 p, %1, 0;\n\t"
-      "bar.red.and.pred q, 1, %2, p;\n\t"
+      "bar.red.and.pred q, %2, %3, p;\n\t"
       "selp.u32 %0, 1, 0, q;\n\t}"
       : "=r"(r)
-      : "r"((uint32_t)ok), "n"(kSoft)
+      : "r"((uint32_t)ok), "r"(1 + group), "n"(kSoft)
       : "memory");
   return r != 0;
 }
@@ -96,8 +100,8 @@ __device__ __forceinline__ uint64_t plain_mn_desc(uint32_t saddr, uint32_t k_byt
   return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(k_bytes >> 4) << 16) | ((uint64_t)(n_bytes >> 4) << 32) | (1ull << 46);
 }
 
-template <int MG>
-__host__ __device__ constexpr int tmem_cols() { return MG <= 4 ? 128 : 256; }
+template <int GROUPS>
+__host__ __device__ constexpr int tmem_cols() { return GROUPS == 1 ? 128 : 256; }
 
 struct Shared {
   uint8_t* base;
@@ -268,9 +272,9 @@ __device__ __forceinline__ void write_q(const Kv8AttnArgs& a, uint8_t* q, float*
 // would have to wait for the softmax, so that they are ready when the softmax is. (Polling for whichever is first
 // took issue slots from the softmax: 98 us instead of 91 for 64 sequences of 8 query heads per KV head.)
 // Lane 0 issues; the warp turns a segment's queries into an operand.
-template <int MG>
+template <int GROUPS>
 __device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
-  constexpr int NP = MG <= 4 ? 16 : 32;
+  constexpr int NP = 16 * GROUPS;
   const uint32_t id_s = idesc_e4m3_f32(128, 16, false, false), id_o = idesc_e4m3_f32(128, NP, true, true);
   const int lane = threadIdx.x & 31;
   uint32_t qk = 0, pv = 0, seg = 0;  // tiles whose scores and whose value products are issued
@@ -289,7 +293,7 @@ __device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, uint32_t 
           continue;
         }
         if (flags & FIRST) {  // the factors of the segment before the last have been read
-          write_q<MG>(a, sh.queries(seg % kStages), sh.factors(seg & 1));
+          write_q<kHeads * GROUPS>(a, sh.queries(seg % kStages), sh.factors(seg & 1));
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(sh.bar(Q_READY + (seg & 1)));
@@ -335,52 +339,37 @@ __device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, uint32_t 
 
 // ------------------------------------------------------------------ softmax and sums (warps 0-3)
 
-template <int MG>
+template <int GROUPS>
 __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
-  constexpr int NP = MG <= 4 ? 16 : 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int NP = 16 * GROUPS;
+  const int group = GROUPS == 1 ? 0 : threadIdx.x / kSoft;
+  const int tid = threadIdx.x % kSoft, lane = tid & 31, warp = tid >> 5;
   const uint32_t tm = tmem + ((uint32_t)(warp * 32) << 16);
-  float* wmax = reinterpret_cast<float*>(sh.base + Layout::kOffMax);
-  float* red = reinterpret_cast<float*>(sh.base + Layout::kOffRed);
-  const int G = a.G;
+  float* wmax = reinterpret_cast<float*>(sh.base + Layout::kOffMax) + group * 32;
+  float* red = reinterpret_cast<float*>(sh.base + Layout::kOffRed) + group * 16;
+  const int g0 = group * kHeads, G = min(kHeads, a.G - g0);  // the group's query heads g0 .. g0 + G - 1
   uint32_t seg = 0;
   bool ok = true;
   auto wait = [&](int bar, uint32_t parity) {
     if (ok && !(ok = mbar_wait(sh.bar(bar), parity, sh.abort_flag()))) give_up(sh);
   };
-  float qs[MG], m[MG], l[MG], acc[MG];
-  float old[MG], now[MG], vs0, vs1;  // what the tile whose value product is under way is added with
+  float qs[kHeads], m[kHeads], l[kHeads], acc[kHeads];
+  float old[kHeads], now[kHeads], vs0, vs1;  // what the tile whose value product is under way is added with
   auto add_values = [&](uint32_t i) {
     wait(O_FULL + (i & 1), (i >> 1) & 1);
     tc_fence_after();
-    if constexpr (MG <= 4) {
-      uint32_t d[32];
-      tmem_ld32(tm + kColO + (i & 1) * 32, d);
-      tmem_ld_wait();
+    uint32_t d[2][16];
 #pragma unroll
-      for (int g = 0; g < MG; ++g) {
-        float o[2];
+    for (int y = 0; y < 2; ++y) tmem_ld16(tm + kColO + ((i & 1) * 2 + y) * NP + group * 16, d[y]);
+    tmem_ld_wait();
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
-          o[y] = fmaf(__uint_as_float(d[16 * y + 8 + g]), 1.f / 1024.f,
-                      fmaf(__uint_as_float(d[16 * y + 4 + g]), 1.f / 32.f, __uint_as_float(d[16 * y + g])));
-        acc[g] = fmaf(acc[g], old[g], fmaf(o[0], vs0, o[1] * vs1) * (now[g] * (1.f / 256.f)));
-      }
-    } else {
-      float o[MG];
+    for (int g = 0; g < kHeads; ++g) {
+      float o[2];
 #pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        uint32_t d[32];
-        tmem_ld32(tm + kColO + ((i & 1) * 2 + y) * NP, d);
-        tmem_ld_wait();
-#pragma unroll
-        for (int g = 0; g < MG; ++g) {
-          const float v = fmaf(__uint_as_float(d[16 + g]), 1.f / 1024.f,
-                               fmaf(__uint_as_float(d[8 + g]), 1.f / 32.f, __uint_as_float(d[g])));
-          if (y == 0) o[g] = v * vs0;
-          else acc[g] = fmaf(acc[g], old[g], fmaf(v, vs1, o[g]) * (now[g] * (1.f / 256.f)));
-        }
-      }
+      for (int y = 0; y < 2; ++y)
+        o[y] = fmaf(__uint_as_float(d[y][8 + g]), 1.f / 1024.f,
+                    fmaf(__uint_as_float(d[y][4 + g]), 1.f / 32.f, __uint_as_float(d[y][g])));
+      acc[g] = fmaf(acc[g], old[g], fmaf(o[0], vs0, o[1] * vs1) * (now[g] * (1.f / 256.f)));
     }
   };
   for (uint32_t it = 0;; ++it) {
@@ -389,7 +378,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
     Meta meta = *sh.meta(s);
     if (!ok) meta.flags = 0;
     if (meta.flags & END) {
-      soft_all(ok);
+      soft_all(group, ok);
       break;
     }
     if (meta.flags & FIRST) {
@@ -397,8 +386,8 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
       wait(Q_READY + buf, (seg >> 1) & 1);
       ++seg;
 #pragma unroll
-      for (int g = 0; g < MG; ++g) {
-        qs[g] = g < G ? sh.factors(buf)[g] : 0.f;
+      for (int g = 0; g < kHeads; ++g) {
+        qs[g] = g < G ? sh.factors(buf)[g0 + g] : 0.f;
         m[g] = -CUDART_INF_F;
         l[g] = acc[g] = 0.f;
       }
@@ -410,65 +399,63 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
       const bool seen = t >= meta.lo && t < meta.n && (meta.flags & (OK0 << half));
       wait(S_FULL + (it & 1), (it >> 1) & 1);
       tc_fence_after();
-      float x[MG];
+      float x[kHeads];
       {
-        uint32_t d[16];
-        tmem_ld16(tm + kColS + (it & 1) * 16, d);
+        uint32_t d0[4], d1[4];
+        tmem_ld4(tm + kColS + (it & 1) * 16 + g0, d0);
+        tmem_ld4(tm + kColS + (it & 1) * 16 + 8 + g0, d1);
         tmem_ld_wait();
 #pragma unroll
-        for (int g = 0; g < MG; ++g) {
-          const float dot = fmaf(__uint_as_float(d[8 + g]), 1.f / 32.f, __uint_as_float(d[g]));
+        for (int g = 0; g < kHeads; ++g) {
+          const float dot = fmaf(__uint_as_float(d1[g]), 1.f / 32.f, __uint_as_float(d0[g]));
           x[g] = seen ? dot * (qs[g] * ks) : -CUDART_INF_F;
         }
       }
-      float* wm = wmax + (it & 1) * 32;
+      float* wm = wmax + (it & 1) * 16;
 #pragma unroll
-      for (int g = 0; g < MG; ++g) {
+      for (int g = 0; g < kHeads; ++g) {
         const float top = warp_max(x[g]);
-        if (lane == g) wm[warp * 8 + g] = top;
+        if (lane == g) wm[warp * 4 + g] = top;
       }
-      if (!soft_all(ok)) break;  // after a failed wait all leave together: nobody is left at a barrier
-      float p[MG], old_next[MG], now_next[MG];
+      if (!soft_all(group, ok)) break;  // after a failed wait all leave together: nobody is left at a barrier
+      float p[kHeads], old_next[kHeads], now_next[kHeads], top[kHeads];
+      {
+        float4 w[4];
 #pragma unroll
-      for (int g = 0; g < MG; ++g) {
-        const float top = fmaxf(fmaxf(wm[g], wm[8 + g]), fmaxf(wm[16 + g], wm[24 + g]));
-        const bool none = top == -CUDART_INF_F;
-        p[g] = exp2f(x[g] - (none ? 0.f : top));
-        const float mn = fmaxf(m[g], top);
+        for (int y = 0; y < 4; ++y) w[y] = reinterpret_cast<const float4*>(wm)[y];
+        top[0] = fmaxf(fmaxf(w[0].x, w[1].x), fmaxf(w[2].x, w[3].x));
+        top[1] = fmaxf(fmaxf(w[0].y, w[1].y), fmaxf(w[2].y, w[3].y));
+        top[2] = fmaxf(fmaxf(w[0].z, w[1].z), fmaxf(w[2].z, w[3].z));
+        top[3] = fmaxf(fmaxf(w[0].w, w[1].w), fmaxf(w[2].w, w[3].w));
+      }
+#pragma unroll
+      for (int g = 0; g < kHeads; ++g) {
+        const bool none = top[g] == -CUDART_INF_F;
+        p[g] = exp2_ftz(x[g] - (none ? 0.f : top[g]));
+        const float mn = fmaxf(m[g], top[g]);
         const float ref = mn == -CUDART_INF_F ? 0.f : mn;
-        old_next[g] = exp2f(m[g] - ref);
-        now_next[g] = none ? 0.f : exp2f(top - ref);
+        old_next[g] = exp2_ftz(m[g] - ref);
+        now_next[g] = none ? 0.f : exp2_ftz(top[g] - ref);
         m[g] = mn;
         l[g] = fmaf(l[g], old_next[g], p[g] * now_next[g]);
       }
-      // the terms of p: two heads to a conversion
-      uint32_t term[3][MG / 2];
+      // the terms of p, two heads at a time: p to the 11 bits of fp16, of which each term takes four
+      uint32_t term[3][kHeads / 2];
 #pragma unroll
-      for (int g = 0; g < MG; g += 2) {
-        float r0 = p[g] * 256.f, r1 = p[g + 1] * 256.f;
+      for (int g = 0; g < kHeads; g += 2) {
+        __half2 r = __floats2half2_rn(p[g] * 256.f, p[g + 1] * 256.f);
 #pragma unroll
         for (int e = 0; e < 3; ++e) {
-          term[e][g / 2] = e4m3x2(r0, r1);
-          if (e < 2) {
-            const float2 v = e4m3x2_value(term[e][g / 2]);
-            r0 = (r0 - v.x) * 32.f;
-            r1 = (r1 - v.y) * 32.f;
-          }
+          term[e][g / 2] = e4m3x2(r);
+          if (e < 2) r = __hmul2(__hsub2(r, e4m3x2_half2(term[e][g / 2])), __float2half2_rn(32.f));  // both exact
         }
       }
-      uint4* prow = reinterpret_cast<uint4*>(sh.weights(it & 1)) + tid;
-      if constexpr (MG <= 4) {
-        *prow = make_uint4(term[0][0] | (term[0][1] << 16), term[1][0] | (term[1][1] << 16),
-                           term[2][0] | (term[2][1] << 16), 0u);
-      } else {
-        prow[0] = make_uint4(term[0][0] | (term[0][1] << 16), term[0][2] | (term[0][3] << 16),
-                             term[1][0] | (term[1][1] << 16), term[1][2] | (term[1][3] << 16));
-        prow[kTileTokens] = make_uint4(term[2][0] | (term[2][1] << 16), term[2][2] | (term[2][3] << 16), 0u, 0u);
-      }
+      reinterpret_cast<uint4*>(sh.weights(it & 1))[group * kTileTokens + tid] =
+          make_uint4(term[0][0] | (term[0][1] << 16), term[1][0] | (term[1][1] << 16), term[2][0] | (term[2][1] << 16), 0u);
       if (meta.t0 < meta.lo || meta.t0 + kTileTokens > meta.n || !both) {
         // value rows outside the attended tokens may hold anything, NaN codes among it
         wait(V_FULL + s, ph);
-        if (!seen) {
+        if (!seen && group == 0) {
           uint4* row = reinterpret_cast<uint4*>(sh.values(s) + tid * kHd);
 #pragma unroll
           for (int c = 0; c < kHd / 16; ++c) row[c] = make_uint4(0u, 0u, 0u, 0u);
@@ -480,7 +467,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
       if (lane == 0) mbar_arrive(sh.bar(P_READY + (it & 1)));
       if (!(meta.flags & FIRST)) add_values(it - 1);
 #pragma unroll
-      for (int g = 0; g < MG; ++g) {
+      for (int g = 0; g < kHeads; ++g) {
         old[g] = old_next[g];
         now[g] = now_next[g];
       }
@@ -490,35 +477,35 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
     if (!(meta.flags & LAST)) continue;
     add_values(it);
     // the sums of p are spread over the threads
-    const size_t row0 = (size_t)meta.head * G;
+    const size_t row0 = (size_t)meta.head * a.G + g0;
 #pragma unroll
-    for (int g = 0; g < MG; ++g) {
+    for (int g = 0; g < kHeads; ++g) {
       const float v = warp_sum(l[g]);
-      if (lane == 0) red[warp * 8 + g] = v;
+      if (lane == 0) red[warp * 4 + g] = v;
     }
-    soft_sync();
+    soft_sync(group);
 #pragma unroll
-    for (int g = 0; g < MG; ++g) l[g] = (red[g] + red[8 + g]) + (red[16 + g] + red[24 + g]);
+    for (int g = 0; g < kHeads; ++g) l[g] = (red[g] + red[4 + g]) + (red[8 + g] + red[12 + g]);
 
     if (!(meta.flags & WHOLE)) {
       float* slot = a.part + (size_t)meta.slot * a.part_stride;
 #pragma unroll
-      for (int g = 0; g < MG; ++g) {
+      for (int g = 0; g < kHeads; ++g) {
         if (g >= G) break;
-        slot[g * kHd + tid] = acc[g];
+        slot[(g0 + g) * kHd + tid] = acc[g];
         if (tid == 0) {
-          slot[G * kHd + g] = m[g];
-          slot[G * kHd + 8 + g] = l[g];
+          slot[a.G * kHd + g0 + g] = m[g];
+          slot[a.G * kHd + 8 + g0 + g] = l[g];
         }
       }
     } else {
-      Joined j[MG];
+      Joined j[kHeads];
 #pragma unroll
-      for (int g = 0; g < MG; ++g)
+      for (int g = 0; g < kHeads; ++g)
         if (g < G) j[g] = join_prev(a, row0 + g, m[g], l[g]);
-      soft_sync();  // lse may be lse_prev: every thread has read it
+      soft_sync(group);  // lse may be lse_prev: every thread has read it
 #pragma unroll
-      for (int g = 0; g < MG; ++g) {
+      for (int g = 0; g < kHeads; ++g) {
         if (g >= G) break;
         ((__nv_bfloat16*)a.o)[(row0 + g) * kHd + tid] = joined_value<__nv_bfloat16>(a, row0 + g, tid, j[g], acc[g]);
         if (a.lse && tid == 0) a.lse[row0 + g] = j[g].lse;
@@ -527,8 +514,8 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
   }
 }
 
-template <int MG>
-__global__ void __launch_bounds__(kThreads, 2)
+template <int GROUPS>
+__global__ void __launch_bounds__(threads_of(GROUPS), 2)
 kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const Kv8AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
@@ -547,7 +534,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     for (int i = 0; i < 2; ++i) {
       mbar_init(sh.bar(Q_READY + i), 1);
       mbar_init(sh.bar(S_FULL + i), 1);
-      mbar_init(sh.bar(P_READY + i), kSoft / 32);
+      mbar_init(sh.bar(P_READY + i), GROUPS * kSoft / 32);
       mbar_init(sh.bar(O_FULL + i), 1);
     }
     mbar_init(sh.bar(DRAIN), 1);
@@ -555,45 +542,46 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     *sh.err() = 0;
     fence_mbar_init();
   }
-  if (warp == 4 && lane == 0) {
+  constexpr int kLoads = GROUPS * kSoft / 32, kIssue = kLoads + 1;
+  if (warp == kLoads && lane == 0) {
     tma_prefetch_desc(&mk);
     tma_prefetch_desc(&mv);
   }
-  if (warp == 5) {
-    tmem_alloc(tmem_holder, tmem_cols<MG>());
+  if (warp == kIssue) {
+    tmem_alloc(tmem_holder, tmem_cols<GROUPS>());
     tmem_relinquish();
   }
   tc_fence_before();
   grid_dependency();
-  const Work wk = find_work<kThreads>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
+  const Work wk = find_work<threads_of(GROUPS)>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
-  if (warp < 4) {
-    attend<MG>(a, sh, tmem);
-  } else if (warp == 4) {
+  if (warp < kLoads) {
+    attend<GROUPS>(a, sh, tmem);
+  } else if (warp == kLoads) {
     load_tiles(a, sh, &mk, &mv, wk);
   } else {
-    issue_products<MG>(a, sh, tmem);
+    issue_products<GROUPS>(a, sh, tmem);
   }
   __syncwarp();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 5) tmem_dealloc(tmem, tmem_cols<MG>());
+  if (warp == kIssue) tmem_dealloc(tmem, tmem_cols<GROUPS>());
   if (threadIdx.x == 0) a.cta_err[blockIdx.x] = *sh.err();
 }
 
-template <int MG>
+template <int GROUPS>
 cudaError_t launch(const Kv8AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
-  const cudaError_t e = cudaFuncSetAttribute(kv8_attn_tc_kernel<MG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout::kBytes);
+  const cudaError_t e = cudaFuncSetAttribute(kv8_attn_tc_kernel<GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kv8_attn_tc_kernel<MG>, dim3(a.n_cta), kThreads, Layout::kBytes, st, mk, mv, a);
+  return launch_overlapped(kv8_attn_tc_kernel<GROUPS>, dim3(a.n_cta), threads_of(GROUPS), Layout::kBytes, st, mk, mv, a);
 }
 
 }  // namespace
 
 cudaError_t launch_attn_tc(const Kv8AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
-  return a.G <= 4 ? launch<4>(a, mk, mv, st) : launch<8>(a, mk, mv, st);
+  return a.G <= kHeads ? launch<1>(a, mk, mv, st) : launch<2>(a, mk, mv, st);
 }
 
 }  // namespace kv8

@@ -20,12 +20,19 @@ __device__ __forceinline__ uint32_t e4m3x2(float lo, float hi) {
   return r;
 }
 
+__device__ __forceinline__ uint32_t e4m3x2(__half2 v) {
+  uint16_t r;
+  asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(*reinterpret_cast<const uint32_t*>(&v)));
+  return r;
+}
+
 // The values of two e4m3 codes (exact in fp16).
-__device__ __forceinline__ float2 e4m3x2_value(uint32_t codes) {
+__device__ __forceinline__ __half2 e4m3x2_half2(uint32_t codes) {
   uint32_t h;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"((uint16_t)codes));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+  return *reinterpret_cast<const __half2*>(&h);
 }
+__device__ __forceinline__ float2 e4m3x2_value(uint32_t codes) { return __half22float2(e4m3x2_half2(codes)); }
 
 // Waits for the grid before in the stream, then lets the next one be launched: what that one reads before
 // its own wait was complete before this grid went on.
@@ -50,6 +57,13 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
+// 2^x; -inf gives 0, results under 2^-126 too.
+__device__ __forceinline__ float exp2_ftz(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // ------------------------------------------------------------------ attention: the division of work
 //
 // A segment is one (sequence, KV head); its tokens are cut into tiles of two pages. The segments, in
@@ -64,7 +78,7 @@ cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size
 
 constexpr int kTilePages = 2;
 constexpr int kTileTokens = kTilePages * kBlock;
-constexpr int kSegmentUnits = 1;
+constexpr int kSegmentUnits = 2;
 
 struct Span {
   int lo, n;        // tokens [lo, n) are attended
@@ -81,6 +95,12 @@ __device__ __forceinline__ Span seq_span(const Kv8AttnArgs& a, int b) {
   s.tiles = s.n == 0 ? 0 : ((s.n + kBlock - 1) / kBlock - s.page0 + kTilePages - 1) / kTilePages;
   s.units = s.n == 0 ? 0 : s.tiles + kSegmentUnits;
   return s;
+}
+
+// First unit of CTA c's range.
+__device__ __forceinline__ long long range_begin(long long total, int c, int active) {
+  if (total <= INT_MAX / 2048) return (unsigned)total * (unsigned)c / (unsigned)active;  // active <= 1024: no 64-bit division
+  return total * c / active;
 }
 
 // A CTA's range of units and where it starts.
@@ -121,8 +141,8 @@ __device__ __forceinline__ Work find_work(const Kv8AttnArgs& a, long long* scrat
   wk.active = (int)min((long long)a.n_cta, total);
   const int c = blockIdx.x;
   const bool has = c < wk.active;
-  wk.begin = has ? total * c / wk.active : 0;
-  wk.end = has ? total * (c + 1) / wk.active : 0;
+  wk.begin = has ? range_begin(total, c, wk.active) : 0;
+  wk.end = has ? range_begin(total, c + 1, wk.active) : 0;
   if (has && wk.begin >= first && wk.begin < first + mine) {
     long long at = first;
     for (int b = b0; b < b1; ++b) {
@@ -144,6 +164,7 @@ __device__ __forceinline__ Work find_work(const Kv8AttnArgs& a, long long* scrat
 // The CTA whose range holds unit t, for total units over `active` CTAs: largest c with
 // c * total / active <= t.
 __device__ __forceinline__ int cta_of_unit(long long t, long long total, int active) {
+  if (total <= INT_MAX / 2048) return (int)(((unsigned)(t + 1) * (unsigned)active - 1) / (unsigned)total);
   return (int)(((t + 1) * active - 1) / total);
 }
 
@@ -246,7 +267,7 @@ __device__ __forceinline__ Pieces pieces_of(const Walk& k) {
   const int active = k.wk.active;
   p.c0 = cta_of_unit(k.seg_first, total, active);
   p.n = cta_of_unit(k.seg_first + k.sp.tiles - 1, total, active) - p.c0 + 1;
-  p.mid = total * p.c0 / active < k.seg_first;
+  p.mid = range_begin(total, p.c0, active) < k.seg_first;
   return p;
 }
 

@@ -313,32 +313,61 @@ class Kv8Pages:
         if n_pages > 1 and v_codes.stride(0) != stride:
             raise ValueError("k_codes and v_codes must have the same distance between pages")
         self.device, self.dtype = k_codes.device, dtype
+        self._index = k_codes.get_device()
         self.batch, self.n_kv_heads, self.head_dim = page_table.shape[0], hkv, hd
         self.c = lr_kv8_pages(self.batch, hkv, hd, n_pages, page_table.shape[1], _DT[dtype], stride, *codes,
                               _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(lens))
         self.ref = ctypes.byref(self.c)
 
+    # These run on every call of a decode step: plain comparisons of a tensor's type, device index and shape.
     def _rows(self, t, n_rows, n_heads, name):
-        """A [n_rows, n_heads, hd] tensor of the cache's dtype and device."""
-        if t.dtype != self.dtype or t.device != self.device or tuple(t.shape) != (n_rows, n_heads, self.head_dim):
+        """Address of a [n_rows, n_heads, hd] tensor of the cache's dtype and device, and its strides."""
+        if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != (n_rows, n_heads, self.head_dim):
             raise ValueError(f"{name} must be a {self.dtype} tensor [{n_rows}, {n_heads}, {self.head_dim}] on {self.device}")
-        return t
+        return t.data_ptr() or None, t.stride()
+
+    def _dense_rows(self, t, n_rows, n_heads, name):
+        ptr = self._rows(t, n_rows, n_heads, name)[0]
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        return ptr
+
+    def _token_rows(self, t, n_rows, n_heads, name):
+        """(address, elements from one token to the next, 0 for one token): the rows of a token are dense."""
+        ptr, (token, head, dim) = self._rows(t, n_rows, n_heads, name)
+        if self.head_dim > 1 and dim != 1 or n_heads > 1 and head != self.head_dim:
+            raise ValueError(f"{name}: the heads of a token must be contiguous")
+        if n_rows < 2:
+            return ptr, 0
+        if token < n_heads * self.head_dim:
+            raise ValueError(f"{name}: the rows of two tokens must not overlap")
+        return ptr, token
 
     def _beside(self, t, dtype, shape, name):
-        if t is not None and (t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape):
-            raise ValueError(f"{name} must be a {dtype} tensor {list(shape)} on {self.device}")
-        return _ptr(t)
+        if t is None:
+            return None
+        if t.dtype is not dtype or t.get_device() != self._index or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {self.device}")
+        return t.data_ptr() or None
 
     def _call(self, entry, args, ws, stream):
         """Run an entry point on the cache's device, on its current stream unless one is given."""
-        if ws is not None and ws.device != self.device:
-            raise ValueError(f"the workspace must live on {self.device}")
-        tail = (_ptr(ws), 0 if ws is None else ws.numel() * ws.element_size())
-        if torch.cuda.current_device() == self.device.index:
-            _check(entry(*args, *tail, _stream(stream)))
+        if ws is None:
+            tail = (None, 0)
+        else:
+            if ws.get_device() != self._index:
+                raise ValueError(f"the workspace must live on {self.device}")
+            tail = (_ptr(ws), ws.numel() * ws.element_size())
+        if torch.cuda.current_device() == self._index:
+            _check(entry(*args, *tail, self._stream(stream)))
         else:
             with torch.cuda.device(self.device):
-                _check(entry(*args, *tail, _stream(stream)))
+                _check(entry(*args, *tail, self._stream(stream)))
+
+    def _stream(self, stream):
+        if stream is None:
+            return torch._C._cuda_getCurrentRawStream(self._index) or None
+        return getattr(stream, "cuda_stream", stream) or None
 
 
 class Rope:
@@ -350,14 +379,7 @@ class Rope:
         self.inv_freq = inv_freq
         self.c = lr_rope(_ptr(inv_freq), int(rot_dim), int(interleaved))
         self.ref = ctypes.byref(self.c)
-
-
-def _token_stride(t, name):
-    """Distance between the token rows of a [n, heads, hd] view whose rows are dense (0 for one row)."""
-    n, heads, hd = t.shape
-    if hd > 1 and t.stride(2) != 1 or heads > 1 and t.stride(1) != hd:
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.stride(0) if n > 1 else 0
+        self.index = inv_freq.get_device()
 
 
 def lr_kv8_append_workspace_bytes(kv: Kv8Pages) -> int:
@@ -370,21 +392,21 @@ def lr_kv8_append(kv: Kv8Pages, k, v, ws, cu_tokens=None, rope: Optional[Rope] =
     queries q [n, Hq, hd] -> q_out rotated by position. k, v and q may be slices of one fused tensor.
     cu_tokens [B + 1] int32 gives each sequence's rows; without it every sequence has one."""
     n = k.shape[0]
-    kv._rows(k, n, kv.n_kv_heads, "k")
-    kv._rows(v, n, kv.n_kv_heads, "v")
+    k_ptr, k_stride = kv._token_rows(k, n, kv.n_kv_heads, "k")
+    v_ptr, v_stride = kv._token_rows(v, n, kv.n_kv_heads, "v")
     hq, q_ptr, q_stride, out_ptr = 0, None, 0, None
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out go together")
     if q is not None:
         hq = q.shape[1]
-        q_ptr, q_stride = kv._rows(q, n, hq, "q").data_ptr() or None, _token_stride(q, "q")
-        out_ptr = _ptr(kv._rows(q_out, n, hq, "q_out"))
-    if rope is not None and rope.inv_freq.device != kv.device:
+        q_ptr, q_stride = kv._token_rows(q, n, hq, "q")
+        out_ptr = kv._dense_rows(q_out, n, hq, "q_out")
+    if rope is not None and rope.index != kv._index:
         raise ValueError(f"inv_freq must live on {kv.device}")
     cu = kv._beside(cu_tokens, torch.int32, (kv.batch + 1,), "cu_tokens")
     kv._call(library().lr_kv8_append,
-             (kv.ref, hq, n, cu, None if rope is None else rope.ref, q_ptr, q_stride, k.data_ptr() or None,
-              _token_stride(k, "k"), v.data_ptr() or None, _token_stride(v, "v"), out_ptr), ws, stream)
+             (kv.ref, hq, n, cu, None if rope is None else rope.ref, q_ptr, q_stride, k_ptr, k_stride, v_ptr, v_stride,
+              out_ptr), ws, stream)
 
 
 def lr_kv8_attn_workspace_bytes(kv: Kv8Pages, n_q_heads: int) -> int:
@@ -398,11 +420,11 @@ def lr_decode_attn_kv8(kv: Kv8Pages, n_q_heads, q, o, ws, lse=None, window=0, sc
                        stream=None) -> None:
     """One decode step over the 8-bit paged cache: q, o [B, Hq, hd]; lse [B, Hq] fp32 (optional);
     o_prev, lse_prev: an earlier partial result over other tokens, joined to the same softmax."""
-    b = kv.batch
-    args = (kv.ref, n_q_heads, _ptr(kv._rows(q, b, n_q_heads, "q")), int(window), float(scale),
-            None if o_prev is None else _ptr(kv._rows(o_prev, b, n_q_heads, "o_prev")),
-            kv._beside(lse_prev, torch.float32, (b, n_q_heads), "lse_prev"),
-            _ptr(kv._rows(o, b, n_q_heads, "o")), kv._beside(lse, torch.float32, (b, n_q_heads), "lse"))
+    b, shape = kv.batch, (kv.batch, n_q_heads)
+    args = (kv.ref, n_q_heads, kv._dense_rows(q, b, n_q_heads, "q"), int(window), float(scale),
+            None if o_prev is None else kv._dense_rows(o_prev, b, n_q_heads, "o_prev"),
+            kv._beside(lse_prev, torch.float32, shape, "lse_prev"),
+            kv._dense_rows(o, b, n_q_heads, "o"), kv._beside(lse, torch.float32, shape, "lse"))
     kv._call(library().lr_decode_attn_kv8, args, ws, stream)
 
 

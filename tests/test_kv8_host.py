@@ -104,9 +104,9 @@ def test_null_cache_and_lse(lib):
 
 
 def _divide(tiles, n_cta):
-    """The attention's division of the segments' tiles, as its kernels do it (a segment takes one unit more than
+    """The attention's division of the segments' tiles, as its kernels do it (a segment takes two units more than
     it has tiles): (CTA, first, last + 1) pieces of every segment, and the pieces' slots."""
-    units = [t + 1 if t else 0 for t in tiles]
+    units = [t + 2 if t else 0 for t in tiles]
     total, active = sum(units), min(n_cta, sum(units))
     first = [sum(units[:i]) for i in range(len(tiles))]
     pieces = {i: [] for i in range(len(tiles))}
@@ -116,7 +116,7 @@ def _divide(tiles, n_cta):
         while at < end:
             s = max(i for i in range(len(tiles)) if tiles[i] and first[i] <= at)
             stop = min(first[s] + tiles[s], end)
-            if stop <= at:  # only the unit behind the tiles
+            if stop <= at:  # only units behind the tiles
                 at = first[s] + units[s]
                 continue
             whole = at == first[s] and stop == first[s] + tiles[s]
