@@ -235,10 +235,16 @@ __global__ void __launch_bounds__(32 * kOneWarps) kv8_append_one_kernel(Kv8Appen
 
 // ------------------------------------------------------------------ ranges of tokens
 //
-// One CTA per page that receives tokens, for a share (blockIdx.y) of the heads. The CTA's threads are
-// 32 rows x hd / 16 pairs of 8-number chunks; a thread has two rows of the page (r and r + 32) and
-// two chunks of each head's row that its rotation pairs up. The angles depend on row and chunk
-// alone, so a thread finds its 16 sines and cosines once and uses them for every head.
+// One CTA per page that receives tokens, for a share (blockIdx.y) of the heads. A thread has one row of the
+// page (64 rows x hd / 16 threads) and, of each head's row, the two chunks of 8 numbers that its rotation
+// pairs up. The angles depend on row and chunk alone, so a thread finds its 8 sines and cosines once and
+// uses them for every head.
+//
+// Bound by memory, if enough of it is asked for in time: a thread copies its own chunks to shared memory
+// with cp.async, kAhead heads ahead (query heads first, then a key and a value row per KV head), and reads
+// them back without a barrier. Keys and values meet at one barrier per KV head, for the largest magnitude.
+// That maximum is taken without a look at what is infinite (NaN drops out by itself); only a page where it
+// comes out infinite is gone through again.
 //
 // Sequence b's pages are the units from cu[b] / 64 + 2 b on: always enough of them (n tokens touch
 // at most n / 64 + 2 pages), without a scan over the batch.
@@ -248,8 +254,7 @@ struct Row8;  // 8 consecutive numbers
 template <>
 struct Row8<__nv_bfloat16> {
   uint4 u;
-  __device__ __forceinline__ void load(const __nv_bfloat16* p) { u = *reinterpret_cast<const uint4*>(p); }
-  __device__ __forceinline__ void zero() { u = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ void from(const uint4* at, int) { u = *at; }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
 #pragma unroll
@@ -263,11 +268,10 @@ struct Row8<__nv_bfloat16> {
 template <>
 struct Row8<float> {
   float4 a, b;
-  __device__ __forceinline__ void load(const float* p) {
-    a = reinterpret_cast<const float4*>(p)[0];
-    b = reinterpret_cast<const float4*>(p)[1];
+  __device__ __forceinline__ void from(const uint4* at, int stride) {
+    a = *reinterpret_cast<const float4*>(at);
+    b = *reinterpret_cast<const float4*>(at + stride);
   }
-  __device__ __forceinline__ void zero() { a = b = make_float4(0.f, 0.f, 0.f, 0.f); }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -284,45 +288,110 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {
+__device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {  // numbers or NaN, no infinities
   uint2 u;
-  u.x = codes2(v[0], v[1], inv) | (codes2(v[2], v[3], inv) << 16);
-  u.y = codes2(v[4], v[5], inv) | (codes2(v[6], v[7], inv) << 16);
+  u.x = e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16);
+  u.y = e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16);
   return u;
 }
 
-// Rotates a thread's two chunks: across them (halves) or within each (interleaved).
-__device__ __forceinline__ void rotate8(bool interleaved, float (&x)[8], float (&y)[8], const float (&s)[8],
-                                        const float (&c)[8]) {
-  if (interleaved) {
+// Rotates across two chunks (halves of the rotated dims), or the pairs within one (interleaved).
+__device__ __forceinline__ void rotate_across(float (&x)[8], float (&y)[8], const float (&s)[8], const float (&c)[8]) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float a0 = x[2 * i], a1 = x[2 * i + 1], b0 = y[2 * i], b1 = y[2 * i + 1];
-      x[2 * i] = a0 * c[i] - a1 * s[i];
-      x[2 * i + 1] = a1 * c[i] + a0 * s[i];
-      y[2 * i] = b0 * c[4 + i] - b1 * s[4 + i];
-      y[2 * i + 1] = b1 * c[4 + i] + b0 * s[4 + i];
-    }
-  } else {
+  for (int i = 0; i < 8; ++i) {
+    const float a0 = x[i], a1 = y[i];
+    x[i] = a0 * c[i] - a1 * s[i];
+    y[i] = a1 * c[i] + a0 * s[i];
+  }
+}
+template <int AT>
+__device__ __forceinline__ void rotate_within(float (&x)[8], const float (&s)[8], const float (&c)[8]) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float a0 = x[i], a1 = y[i];
-      x[i] = a0 * c[i] - a1 * s[i];
-      y[i] = a1 * c[i] + a0 * s[i];
-    }
+  for (int i = 0; i < 4; ++i) {
+    const float a0 = x[2 * i], a1 = x[2 * i + 1];
+    x[2 * i] = a0 * c[AT + i] - a1 * s[AT + i];
+    x[2 * i + 1] = a1 * c[AT + i] + a0 * s[AT + i];
   }
 }
 
 __device__ __forceinline__ int unit_of(const Kv8AppendArgs& a, int b) { return __ldg(a.cu + b) / kBlock + 2 * b; }
 
+// The device checks of every sequence and page, by one CTA: the word is written, so nothing has to clear it
+// before.
+__device__ void check_ranges(const Kv8AppendArgs& a, int n_units, int* bits) {
+  if (threadIdx.x == 0) *bits = 0;
+  __syncthreads();
+  int mine = 0;
+  for (int b = threadIdx.x; b < a.B; b += blockDim.x)
+    if (!new_tokens(a, b).ok) mine |= LR_DEVERR_LEN;
+  for (int u = threadIdx.x; u < n_units; u += blockDim.x) {
+    int b = 0, len = a.B;  // largest b with unit_of(b) <= u
+    while (len > 1) {
+      const int half = len / 2;
+      if (unit_of(a, b + half) <= u) {
+        b += half;
+        len -= half;
+      } else {
+        len = half;
+      }
+    }
+    const NewTokens t = new_tokens(a, b);
+    const int page_i = u - unit_of(a, b), pg = t.p0 / kBlock + page_i;
+    if (page_i >= 0 && t.n && pg * kBlock < t.p0 + t.n &&
+        (unsigned)__ldg(a.table + (size_t)b * a.max_pages + pg) >= (unsigned)a.n_pages)
+      mine |= LR_DEVERR_PAGE;
+  }
+  if (mine) atomicOr(bits, mine);
+  __syncthreads();
+  if (threadIdx.x == 0) *a.err = *bits;
+}
+
+// Largest magnitude of 8 numbers, and of the finite ones alone.
+__device__ __forceinline__ float top8(const Row8<__nv_bfloat16>& v) {
+  const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&v.u);
+  const __nv_bfloat162 zero = __floats2bfloat162_rn(0.f, 0.f);
+  const __nv_bfloat162 m = __hmax2(__hmax2(__hmax2(zero, __habs2(h[0])), __hmax2(zero, __habs2(h[1]))),
+                                   __hmax2(__hmax2(zero, __habs2(h[2])), __hmax2(zero, __habs2(h[3]))));
+  return fmaxf(__low2float(m), __high2float(m));
+}
+__device__ __forceinline__ float top8(const float (&v)[8]) {
+  float m = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
+}
+__device__ __forceinline__ float top8(const Row8<float>& v) {
+  float f[8];
+  v.get(f);
+  return top8(f);
+}
+__device__ __forceinline__ uint32_t finite_top8(const float (&v)[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = max(m, finite_bits(v[i]));
+  return m;
+}
+
+__device__ __forceinline__ void copy16(void* smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global)
+               : "memory");
+}
+
+// Items in shared memory, under way or at work. A key and its value are at work together; four fp32 items
+// would not fit at head_dim 256.
 template <typename T>
-__global__ void __launch_bounds__(512) kv8_append_kernel(Kv8AppendArgs a, int n_units) {
-  __shared__ uint32_t top[2][2][16];  // [parity][key, value][warp]
+constexpr int ahead() { return sizeof(T) == 2 ? 4 : 3; }
+constexpr int kMaxWarps = 32;
+
+template <typename T>
+__global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n_units) {
+  constexpr int kAhead = ahead<T>();
+  extern __shared__ __align__(16) uint8_t ring[];  // [kAhead][2 chunks][16-byte parts][thread]
+  __shared__ uint32_t top[2][2][kMaxWarps];        // [parity][key, value][warp]
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, n_warps = blockDim.x >> 5;
   const int u = blockIdx.x;
-  if (u >= n_units) {  // the device checks of the sequences
-    const int b = (u - n_units) * blockDim.x + tid;
-    if (blockIdx.y == 0 && b < a.B && !new_tokens(a, b).ok) flag_error(a.err, LR_DEVERR_LEN);
+  if (u == n_units) {
+    if (blockIdx.y == 0) check_ranges(a, n_units, (int*)top);
     return;
   }
   // the sequence of this unit: largest b with unit_of(b) <= u, 32 candidates a round
@@ -343,113 +412,138 @@ __global__ void __launch_bounds__(512) kv8_append_kernel(Kv8AppendArgs a, int n_
   const int slot0 = first - pg * kBlock, rows = end - first;  // new rows slot0 .. slot0 + rows - 1
   const int token0 = t.start + (first - t.p0);
   int page = __ldg(a.table + (size_t)b * a.max_pages + pg);
-  if ((unsigned)page >= (unsigned)a.n_pages) {
-    if (tid == 0 && blockIdx.y == 0) flag_error(a.err, LR_DEVERR_PAGE);
-    page = -1;
-  }
+  if ((unsigned)page >= (unsigned)a.n_pages) page = -1;
   const int hd = a.hd, P = (hd + 15) / 16;  // chunk pairs of a row
-  const int r0 = tid / P, p = tid % P;
-  const int rot_pairs = a.rot / 16;
-  int c0, c1;  // the thread's chunks, as first dims
-  if (!a.interleaved && p < rot_pairs) {
-    c0 = 8 * p;
-    c1 = a.rot / 2 + 8 * p;
-  } else {
-    c0 = 16 * p;
-    c1 = 16 * p + 8;
+  const int r = tid / P, p = tid % P;
+  // The thread's chunks, as first dims, so that neighbours in the row are neighbours in the warp: the halves'
+  // pairs and then the rest of the row in two halves, or all of it in two halves.
+  int c0 = 8 * p, c1 = 8 * (P + p);
+  bool across = false;
+  if (!a.interleaved) {
+    const int pairs = a.rot / 16;
+    across = p < pairs;
+    c0 = across ? 8 * p : a.rot + 8 * (p - pairs);
+    c1 = across ? a.rot / 2 + 8 * p : a.rot + 8 * (P - pairs + p - pairs);
   }
-  const bool rotated = p < rot_pairs, two = c1 < hd;  // head_dim an odd multiple of 8: the last chunk is alone
-  float s[2][8], c[2][8];
-  if (rotated) {
+  const bool two = c1 < hd;  // head_dim an odd multiple of 8: one chunk is alone
+  const bool within0 = a.interleaved && c0 < a.rot, within1 = a.interleaved && c1 < a.rot;
+  const bool in = r < rows;
+  const size_t token = (size_t)(token0 + (in ? r : 0));
+
+  // items: this share's query heads, then key and value of its KV heads
+  const int y = blockIdx.y, ny = gridDim.y;
+  const int n_q = a.Hq > y ? (a.Hq - y - 1) / ny + 1 : 0, n_kv = page >= 0 && a.Hkv > y ? (a.Hkv - y - 1) / ny + 1 : 0;
+  const int n_items = n_q + 2 * n_kv;
+  constexpr int kParts = sizeof(T) == 2 ? 1 : 2;  // 16 bytes each
+  uint4* const slots = reinterpret_cast<uint4*>(ring) + tid;
+  auto slot = [&](int item, int chunk, int part) {
+    return slots + (size_t)(((item % kAhead) * 2 + chunk) * kParts + part) * blockDim.x;
+  };
+  auto copy = [&](int item) {
+    if (in && item < n_items) {
+      const T* src;
+      if (item < n_q) {
+        src = (const T*)a.q + token * a.q_stride + (size_t)(y + item * ny) * hd;
+      } else {
+        const size_t h = y + ((item - n_q) >> 1) * ny;
+        src = (item - n_q) & 1 ? (const T*)a.v + token * a.v_stride + h * hd : (const T*)a.k + token * a.k_stride + h * hd;
+      }
+#pragma unroll
+      for (int x = 0; x < kParts; ++x) {
+        copy16(slot(item, 0, x), reinterpret_cast<const uint4*>(src + c0) + x);
+        if (two) copy16(slot(item, 1, x), reinterpret_cast<const uint4*>(src + c1) + x);
+      }
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  auto take = [&](int item, int chunk) {
+    Row8<T> v;
+    v.from(slot(item, chunk, 0), blockDim.x);
+    return v;
+  };
+  for (int i = 0; i < kAhead - 1; ++i) copy(i);
+
+  float s[8], c[8];
+  if (in) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const uint64_t f = turn_fraction(__ldg(a.inv_freq + 8 * p + i));
-#pragma unroll
-      for (int x = 0; x < 2; ++x) sin_cos(f, first + r0 + 32 * x, s[x][i], c[x][i]);
+      if (!(across || (i < 4 ? within0 : within1))) continue;
+      const int pair = across ? c0 + i : i < 4 ? c0 / 2 + i : c1 / 2 + i - 4;
+      sin_cos(turn_fraction(__ldg(a.inv_freq + pair)), first + r, s[i], c[i]);
     }
   }
-  const bool in[2] = {r0 < rows, r0 + 32 < rows};
+  auto rotate = [&](float (&x0)[8], float (&x1)[8]) {
+    if (across) rotate_across(x0, x1, s, c);
+    if (within0) rotate_within<0>(x0, s, c);
+    if (within1) rotate_within<4>(x1, s, c);
+  };
 
   // queries
-  for (int h = blockIdx.y; h < a.Hq; h += gridDim.y) {
-    Row8<T> raw[2][2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (!in[x]) continue;
-      const T* src = (const T*)a.q + (size_t)(token0 + r0 + 32 * x) * a.q_stride + (size_t)h * hd;
-      raw[x][0].load(src + c0);
-      if (two) raw[x][1].load(src + c1);
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (!in[x]) continue;
+  for (int i = 0; i < n_q; ++i) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+    if (in) {
       float v0[8], v1[8] = {};
-      raw[x][0].get(v0);
-      if (two) raw[x][1].get(v1);
-      if (rotated) rotate8(a.interleaved, v0, v1, s[x], c[x]);
-      T* out = (T*)a.q_out + ((size_t)(token0 + r0 + 32 * x) * a.Hq + h) * hd;
+      take(i, 0).get(v0);
+      if (two) take(i, 1).get(v1);
+      rotate(v0, v1);
+      T* out = (T*)a.q_out + (token * a.Hq + y + i * ny) * hd;
       store8(out + c0, v0);
       if (two) store8(out + c1, v1);
     }
+    copy(i + kAhead - 1);
   }
-  if (page < 0) return;
 
   // keys and values
-  int parity = 0;
-  for (int h = blockIdx.y; h < a.Hkv; h += gridDim.y, parity ^= 1) {
-    Row8<T> rk[2][2], rv[2][2];
+  for (int j = 0; j < n_kv; ++j) {
+    const int h = y + j * ny, ki = n_q + 2 * j, parity = j & 1;
     const size_t sc = (size_t)page * a.Hkv + h;
     float held[2] = {0.f, 0.f};
     if (slot0 > 0) {
       held[0] = a.ks[sc];
       held[1] = a.vs[sc];
     }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        rk[x][e].zero();
-        rv[x][e].zero();
-      }
-      if (!in[x]) continue;
-      const size_t tok = (size_t)(token0 + r0 + 32 * x);
-      const T* ksrc = (const T*)a.k + tok * a.k_stride + (size_t)h * hd;
-      const T* vsrc = (const T*)a.v + tok * a.v_stride + (size_t)h * hd;
-      rk[x][0].load(ksrc + c0);
-      rv[x][0].load(vsrc + c0);
-      if (two) {
-        rk[x][1].load(ksrc + c1);
-        rv[x][1].load(vsrc + c1);
-      }
-    }
-    float kx[2][2][8];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 3) : "memory");  // both items
+    float kx[2][8] = {};
     uint32_t mk = 0, mv = 0;
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      rk[x][0].get(kx[x][0]);
-      rk[x][1].get(kx[x][1]);
-      if (rotated) rotate8(a.interleaved, kx[x][0], kx[x][1], s[x], c[x]);
-      float v[8];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        rv[x][e].get(v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          mv = max(mv, finite_bits(v[i]));
-          mk = max(mk, in[x] ? finite_bits(kx[x][e][i]) : 0u);
+    if (in) {
+      take(ki, 0).get(kx[0]);
+      float m = top8(take(ki + 1, 0));
+      if (two) {
+        take(ki, 1).get(kx[1]);
+        m = fmaxf(m, top8(take(ki + 1, 1)));
+      }
+      rotate(kx[0], kx[1]);
+      mk = __float_as_uint(fmaxf(top8(kx[0]), top8(kx[1])));
+      mv = __float_as_uint(m);
+    }
+    auto largest = [&](uint32_t (&row)[2][kMaxWarps], bool again) {
+      mk = __reduce_max_sync(0xffffffffu, mk);
+      mv = __reduce_max_sync(0xffffffffu, mv);
+      if (again) __syncthreads();  // the first maxima have been read
+      if (lane == 0) {
+        row[0][warp] = mk;
+        row[1][warp] = mv;
+      }
+      __syncthreads();
+      mk = __reduce_max_sync(0xffffffffu, lane < n_warps ? row[0][lane] : 0u);
+      mv = __reduce_max_sync(0xffffffffu, lane < n_warps ? row[1][lane] : 0u);
+    };
+    largest(top[parity], false);
+    constexpr uint32_t kInf = 0x7f800000u;
+    const bool infinite = mk >= kInf || mv >= kInf;
+    if (infinite) {  // rare
+      mk = mv = 0;
+      if (in) {
+        float v[8];
+        mk = max(finite_top8(kx[0]), finite_top8(kx[1]));
+        take(ki + 1, 0).get(v);
+        mv = finite_top8(v);
+        if (two) {
+          take(ki + 1, 1).get(v);
+          mv = max(mv, finite_top8(v));
         }
       }
-    }
-    mk = __reduce_max_sync(0xffffffffu, mk);
-    mv = __reduce_max_sync(0xffffffffu, mv);
-    if (lane == 0) {
-      top[parity][0][warp] = mk;
-      top[parity][1][warp] = mv;
-    }
-    __syncthreads();
-    for (int w = 0; w < n_warps; ++w) {
-      mk = max(mk, top[parity][0][w]);
-      mv = max(mv, top[parity][1][w]);
+      largest(top[parity], true);
     }
     const float now[2] = {fmaxf(held[0], pow2(scale_exp(mk))), fmaxf(held[1], pow2(scale_exp(mv)))};
     uint8_t* const head[2] = {a.kc + (size_t)page * a.page_stride + (size_t)h * kBlock * hd,
@@ -465,22 +559,30 @@ __global__ void __launch_bounds__(512) kv8_append_kernel(Kv8AppendArgs a, int n_
       }
       if (tid == e) (e ? a.vs : a.ks)[sc] = now[e];
     }
-    const float ik = 1.f / now[0], iv = 1.f / now[1];
+    if (in) {
+      const float ik = 1.f / now[0], iv = 1.f / now[1];
+      const size_t off = (size_t)(slot0 + r) * hd;
 #pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      if (!in[x]) continue;
-      const size_t off = (size_t)(slot0 + r0 + 32 * x) * hd;
-      float v[8];
-      *reinterpret_cast<uint2*>(head[0] + off + c0) = codes8(kx[x][0], ik);
-      rv[x][0].get(v);
-      *reinterpret_cast<uint2*>(head[1] + off + c0) = codes8(v, iv);
-      if (two) {
-        *reinterpret_cast<uint2*>(head[0] + off + c1) = codes8(kx[x][1], ik);
-        rv[x][1].get(v);
-        *reinterpret_cast<uint2*>(head[1] + off + c1) = codes8(v, iv);
+      for (int x = 0; x < 2; ++x) {
+        if (x && !two) break;
+        float v[8];
+        take(ki + 1, x).get(v);
+        const int at = x ? c1 : c0;
+        if (infinite) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            v[i] = or_nan(v[i]);
+            kx[x][i] = or_nan(kx[x][i]);
+          }
+        }
+        *reinterpret_cast<uint2*>(head[0] + off + at) = codes8(kx[x], ik);
+        *reinterpret_cast<uint2*>(head[1] + off + at) = codes8(v, iv);
       }
     }
+    copy(ki + kAhead - 1);
+    copy(ki + kAhead);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 template <typename T>
@@ -492,14 +594,27 @@ cudaError_t launch_append(const Kv8AppendArgs& a, int sm_count, cudaStream_t st)
     else kv8_append_one_kernel<T, 2><<<grid, 32 * kOneWarps, 0, st>>>(a);
     return cudaGetLastError();
   }
-  const cudaError_t e = cudaMemsetAsync(a.err, 0, 256, st);
+  const int threads = kBlock * ((a.hd + 15) / 16);
+  const int units = a.n_tokens / kBlock + 2 * a.B, pages = a.n_tokens / kBlock + a.B;
+  const int smem = ahead<T>() * 2 * 8 * (int)sizeof(T) * threads;
+  // Heads are shared out among ny CTAs: more of them fill the machine evenly, but each finds the angles
+  // again, which costs about as much as kAngles rows. A page for each sequence's end is counted.
+  constexpr float kAngles = 6.f;
+  const int per_sm = std::max(1, std::min(1024 / threads, 220 * 1024 / smem)), heads = a.Hq + 2 * a.Hkv;
+  int ny = 1;
+  float best = 0.f;
+  for (int y = 1; y <= a.Hkv && y <= 64; ++y) {
+    const long long waves = ((long long)pages * y + (long long)per_sm * sm_count - 1) / ((long long)per_sm * sm_count);
+    const float cost = (float)waves * (kAngles + (float)((heads + y - 1) / y));
+    if (y == 1 || cost < best) {
+      best = cost;
+      ny = y;
+    }
+  }
+  const cudaError_t e = cudaFuncSetAttribute(kv8_append_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  const int threads = 32 * ((a.hd + 15) / 16);
-  const int units = a.n_tokens / kBlock + 2 * a.B;
-  // heads are shared out among CTAs until the grid fills the SMs four times over
-  const int ny = std::min(a.Hkv, std::max(1, 4 * sm_count / std::max(1, units)));
-  const dim3 grid((unsigned)(units + (a.B + threads - 1) / threads), (unsigned)ny);
-  kv8_append_kernel<T><<<grid, threads, 0, st>>>(a, units);
+  const dim3 grid((unsigned)units + 1, (unsigned)ny);  // the last one checks
+  kv8_append_kernel<T><<<grid, threads, smem, st>>>(a, units);
   return cudaGetLastError();
 }
 
