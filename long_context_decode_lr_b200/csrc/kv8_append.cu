@@ -25,9 +25,18 @@ __device__ __forceinline__ uint64_t turn_fraction(float radians) {
   t -= floor(t);
   return (uint64_t)(t * 18446744073709551616.0);
 }
+// T: what the rotated numbers are rounded to. bf16 takes the hardware's sine and cosine (within 2^-21 on one
+// turn, against half a step of 2^-9; with sincospif the angles were a fifth of all instructions).
+template <typename T>
 __device__ __forceinline__ void sin_cos(uint64_t fraction, int pos, float& s, float& c) {
   const int32_t turns = (int32_t)((fraction * (uint64_t)(uint32_t)pos) >> 32);
-  sincospif((float)turns * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+  if constexpr (sizeof(T) == 2) {
+    const float x = (float)turns * 1.4629180792671596e-9f;  // pi 2^-31: radians
+    s = __sinf(x);
+    c = __cosf(x);
+  } else {
+    sincospif((float)turns * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+  }
 }
 
 // Exponent of the smallest power of two s >= 2^-24 with amax <= 448 s (448 = 1.75 * 2^8).
@@ -210,7 +219,7 @@ __global__ void __launch_bounds__(32 * kOneWarps) kv8_append_one_kernel(Kv8Appen
     if (i < a.rot / 4) {
       float s[2], c[2];
 #pragma unroll
-      for (int e = 0; e < 2; ++e) sin_cos(turn_fraction(__ldg(a.inv_freq + 2 * i + e)), t.p0, s[e], c[e]);
+      for (int e = 0; e < 2; ++e) sin_cos<T>(turn_fraction(__ldg(a.inv_freq + 2 * i + e)), t.p0, s[e], c[e]);
       rotate_quad(a.interleaved, x[u], s, c);
     }
   }
@@ -254,7 +263,6 @@ struct Row8;  // 8 consecutive numbers
 template <>
 struct Row8<__nv_bfloat16> {
   uint4 u;
-  __device__ __forceinline__ void from(const uint4* at, int) { u = *at; }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const __nv_bfloat162* h = reinterpret_cast<const __nv_bfloat162*>(&u);
 #pragma unroll
@@ -268,10 +276,6 @@ struct Row8<__nv_bfloat16> {
 template <>
 struct Row8<float> {
   float4 a, b;
-  __device__ __forceinline__ void from(const uint4* at, int stride) {
-    a = *reinterpret_cast<const float4*>(at);
-    b = *reinterpret_cast<const float4*>(at + stride);
-  }
   __device__ __forceinline__ void get(float (&v)[8]) const {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
@@ -372,9 +376,13 @@ __device__ __forceinline__ uint32_t finite_top8(const float (&v)[8]) {
   return m;
 }
 
-__device__ __forceinline__ void copy16(void* smem, const void* global) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"((uint32_t)__cvta_generic_to_shared(smem)), "l"(global)
-               : "memory");
+__device__ __forceinline__ void copy16(uint32_t smem, const void* global) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(global) : "memory");
+}
+__device__ __forceinline__ uint4 load16(uint32_t smem) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem) : "memory");
+  return v;
 }
 
 // Items in shared memory, under way or at work. A key and its value are at work together; four fp32 items
@@ -383,7 +391,11 @@ template <typename T>
 constexpr int ahead() { return sizeof(T) == 2 ? 4 : 3; }
 constexpr int kMaxWarps = 32;
 
-template <typename T>
+// What the rotation does to a thread's chunks. One kernel per answer: asked of every thread and chunk, the
+// question alone was most of the instructions.
+enum class Turn { kNone, kAcross, kWithin, kMixed };  // kMixed: part of the row, or a chunk alone
+
+template <typename T, Turn kTurn>
 __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n_units) {
   constexpr int kAhead = ahead<T>();
   extern __shared__ __align__(16) uint8_t ring[];  // [kAhead][2 chunks][16-byte parts][thread]
@@ -418,84 +430,100 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
   // The thread's chunks, as first dims, so that neighbours in the row are neighbours in the warp: the halves'
   // pairs and then the rest of the row in two halves, or all of it in two halves.
   int c0 = 8 * p, c1 = 8 * (P + p);
-  bool across = false;
-  if (!a.interleaved) {
-    const int pairs = a.rot / 16;
-    across = p < pairs;
-    c0 = across ? 8 * p : a.rot + 8 * (p - pairs);
-    c1 = across ? a.rot / 2 + 8 * p : a.rot + 8 * (P - pairs + p - pairs);
+  bool across = kTurn == Turn::kAcross, within0 = kTurn == Turn::kWithin, within1 = within0, two = true;
+  if (kTurn == Turn::kMixed) {
+    if (!a.interleaved) {
+      const int pairs = a.rot / 16;
+      across = p < pairs;
+      c0 = across ? 8 * p : a.rot + 8 * (p - pairs);
+      c1 = across ? a.rot / 2 + 8 * p : a.rot + 8 * (P - pairs + p - pairs);
+    }
+    two = c1 < hd;  // head_dim an odd multiple of 8: one chunk is alone
+    within0 = a.interleaved && c0 < a.rot;
+    within1 = a.interleaved && c1 < a.rot;
   }
-  const bool two = c1 < hd;  // head_dim an odd multiple of 8: one chunk is alone
-  const bool within0 = a.interleaved && c0 < a.rot, within1 = a.interleaved && c1 < a.rot;
   const bool in = r < rows;
   const size_t token = (size_t)(token0 + (in ? r : 0));
 
   // items: this share's query heads, then key and value of its KV heads
   const int y = blockIdx.y, ny = gridDim.y;
   const int n_q = a.Hq > y ? (a.Hq - y - 1) / ny + 1 : 0, n_kv = page >= 0 && a.Hkv > y ? (a.Hkv - y - 1) / ny + 1 : 0;
-  const int n_items = n_q + 2 * n_kv;
   constexpr int kParts = sizeof(T) == 2 ? 1 : 2;  // 16 bytes each
-  uint4* const slots = reinterpret_cast<uint4*>(ring) + tid;
-  auto slot = [&](int item, int chunk, int part) {
-    return slots + (size_t)(((item % kAhead) * 2 + chunk) * kParts + part) * blockDim.x;
-  };
-  auto copy = [&](int item) {
-    if (in && item < n_items) {
-      const T* src;
-      if (item < n_q) {
-        src = (const T*)a.q + token * a.q_stride + (size_t)(y + item * ny) * hd;
-      } else {
-        const size_t h = y + ((item - n_q) >> 1) * ny;
-        src = (item - n_q) & 1 ? (const T*)a.v + token * a.v_stride + h * hd : (const T*)a.k + token * a.k_stride + h * hd;
-      }
+  const uint32_t part_bytes = blockDim.x * 16, slot_bytes = 2 * kParts * part_bytes;
+  const uint32_t slots = (uint32_t)__cvta_generic_to_shared(ring) + tid * 16;
+  auto copy = [&](int slot, const T* src) {
+    const uint32_t to = slots + slot * slot_bytes;
 #pragma unroll
-      for (int x = 0; x < kParts; ++x) {
-        copy16(slot(item, 0, x), reinterpret_cast<const uint4*>(src + c0) + x);
-        if (two) copy16(slot(item, 1, x), reinterpret_cast<const uint4*>(src + c1) + x);
-      }
+    for (int x = 0; x < kParts; ++x) {
+      copy16(to + x * part_bytes, reinterpret_cast<const uint4*>(src + c0) + x);
+      if (two) copy16(to + (kParts + x) * part_bytes, reinterpret_cast<const uint4*>(src + c1) + x);
     }
-    asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  auto take = [&](int item, int chunk) {
+  auto take = [&](int slot, int chunk) {
+    const uint32_t from = slots + slot * slot_bytes + chunk * kParts * part_bytes;
     Row8<T> v;
-    v.from(slot(item, chunk, 0), blockDim.x);
+    uint4* to = reinterpret_cast<uint4*>(&v);
+#pragma unroll
+    for (int x = 0; x < kParts; ++x) to[x] = load16(from + x * part_bytes);
     return v;
   };
-  for (int i = 0; i < kAhead - 1; ++i) copy(i);
-
-  float s[8], c[8];
-  if (in) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      if (!(across || (i < 4 ? within0 : within1))) continue;
-      const int pair = across ? c0 + i : i < 4 ? c0 / 2 + i : c1 / 2 + i - 4;
-      sin_cos(turn_fraction(__ldg(a.inv_freq + pair)), first + r, s[i], c[i]);
+  // the next item to copy; the queries are counted up to whole rings, so that an item's slot is known
+  const int n_q_ring = (n_q + kAhead - 1) / kAhead * kAhead, n_items = n_q_ring + 2 * n_kv, step = ny * hd;
+  const T* q_next = (const T*)a.q + token * a.q_stride + y * hd;
+  const T* k_next = (const T*)a.k + token * a.k_stride + y * hd;
+  const T* v_next = (const T*)a.v + token * a.v_stride + y * hd;
+  int next = 0;
+  auto copy_next = [&](int slot) {
+    if (next < n_q) {
+      copy(slot, q_next);
+      q_next += step;
+    } else if (next >= n_q_ring && next < n_items) {
+      copy(slot, (next - n_q_ring) & 1 ? v_next : k_next);
+      if ((next - n_q_ring) & 1) v_next += step;
+      else k_next += step;
     }
-  }
+    ++next;
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  };
+  float s[8], c[8];
   auto rotate = [&](float (&x0)[8], float (&x1)[8]) {
     if (across) rotate_across(x0, x1, s, c);
     if (within0) rotate_within<0>(x0, s, c);
     if (within1) rotate_within<4>(x1, s, c);
   };
-
-  // queries
-  for (int i = 0; i < n_q; ++i) {
-    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
-    if (in) {
-      float v0[8], v1[8] = {};
-      take(i, 0).get(v0);
-      if (two) take(i, 1).get(v1);
-      rotate(v0, v1);
-      T* out = (T*)a.q_out + (token * a.Hq + y + i * ny) * hd;
-      store8(out + c0, v0);
-      if (two) store8(out + c1, v1);
+  if (in) {
+#pragma unroll
+    for (int i = 0; i < kAhead - 1; ++i) copy_next(i);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!(across || (i < 4 ? within0 : within1))) continue;
+      const int pair = across ? c0 + i : i < 4 ? c0 / 2 + i : c1 / 2 + i - 4;
+      sin_cos<T>(turn_fraction(__ldg(a.inv_freq + pair)), first + r, s[i], c[i]);
     }
-    copy(i + kAhead - 1);
+    // queries
+    T* out = (T*)a.q_out + (token * a.Hq + y) * hd;
+    for (int i0 = 0; i0 < n_q_ring; i0 += kAhead) {
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 2) : "memory");
+        if (i0 + x < n_q) {
+          float v0[8], v1[8] = {};
+          take(x, 0).get(v0);
+          if (two) take(x, 1).get(v1);
+          rotate(v0, v1);
+          store8(out + c0, v0);
+          if (two) store8(out + c1, v1);
+          out += step;
+        }
+        copy_next((x + kAhead - 1) % kAhead);
+      }
+    }
   }
 
   // keys and values
+  int ks = 0;  // slot of the key
   for (int j = 0; j < n_kv; ++j) {
-    const int h = y + j * ny, ki = n_q + 2 * j, parity = j & 1;
+    const int h = y + j * ny, parity = j & 1, vs = ks + 1 < kAhead ? ks + 1 : 0;
     const size_t sc = (size_t)page * a.Hkv + h;
     float held[2] = {0.f, 0.f};
     if (slot0 > 0) {
@@ -506,11 +534,11 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
     float kx[2][8] = {};
     uint32_t mk = 0, mv = 0;
     if (in) {
-      take(ki, 0).get(kx[0]);
-      float m = top8(take(ki + 1, 0));
+      take(ks, 0).get(kx[0]);
+      float m = top8(take(vs, 0));
       if (two) {
-        take(ki, 1).get(kx[1]);
-        m = fmaxf(m, top8(take(ki + 1, 1)));
+        take(ks, 1).get(kx[1]);
+        m = fmaxf(m, top8(take(vs, 1)));
       }
       rotate(kx[0], kx[1]);
       mk = __float_as_uint(fmaxf(top8(kx[0]), top8(kx[1])));
@@ -536,10 +564,10 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
       if (in) {
         float v[8];
         mk = max(finite_top8(kx[0]), finite_top8(kx[1]));
-        take(ki + 1, 0).get(v);
+        take(vs, 0).get(v);
         mv = finite_top8(v);
         if (two) {
-          take(ki + 1, 1).get(v);
+          take(vs, 1).get(v);
           mv = max(mv, finite_top8(v));
         }
       }
@@ -566,7 +594,7 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
       for (int x = 0; x < 2; ++x) {
         if (x && !two) break;
         float v[8];
-        take(ki + 1, x).get(v);
+        take(vs, x).get(v);
         const int at = x ? c1 : c0;
         if (infinite) {
 #pragma unroll
@@ -579,8 +607,11 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
         *reinterpret_cast<uint2*>(head[1] + off + at) = codes8(v, iv);
       }
     }
-    copy(ki + kAhead - 1);
-    copy(ki + kAhead);
+    if (in) {
+      copy_next(ks ? ks - 1 : kAhead - 1);
+      copy_next(ks);
+    }
+    ks = vs + 1 < kAhead ? vs + 1 : 0;
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
@@ -611,10 +642,14 @@ cudaError_t launch_append(const Kv8AppendArgs& a, int sm_count, cudaStream_t st)
       ny = y;
     }
   }
-  const cudaError_t e = cudaFuncSetAttribute(kv8_append_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  void (*kernel)(Kv8AppendArgs, int) = kv8_append_kernel<T, Turn::kMixed>;
+  if (a.hd % 16 == 0 && a.rot == 0) kernel = kv8_append_kernel<T, Turn::kNone>;
+  else if (a.hd % 16 == 0 && a.rot == a.hd)
+    kernel = a.interleaved ? kv8_append_kernel<T, Turn::kWithin> : kv8_append_kernel<T, Turn::kAcross>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
   const dim3 grid((unsigned)units + 1, (unsigned)ny);  // the last one checks
-  kv8_append_kernel<T><<<grid, threads, smem, st>>>(a, units);
+  kernel<<<grid, threads, smem, st>>>(a, units);
   return cudaGetLastError();
 }
 
