@@ -292,30 +292,53 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
+// Two fp32 operations in one instruction.
+struct Two {
+  uint64_t v;
+  __device__ __forceinline__ Two() {}
+  __device__ __forceinline__ Two(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {  // numbers or NaN, no infinities
   uint2 u;
-  u.x = e4m3x2(v[0] * inv, v[1] * inv) | (e4m3x2(v[2] * inv, v[3] * inv) << 16);
-  u.y = e4m3x2(v[4] * inv, v[5] * inv) | (e4m3x2(v[6] * inv, v[7] * inv) << 16);
+  const Two f(inv, inv);
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) mul(Two(v[i], v[i + 1]), f).get(x[i], x[i + 1]);
+  u.x = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
+  u.y = e4m3x2(x[4], x[5]) | (e4m3x2(x[6], x[7]) << 16);
   return u;
 }
 
+// Sines, negative sines and cosines of a thread's 8 angles.
+struct Angles {
+  Two s[4], n[4], c[4];
+};
+// Two pairs (x, y) turned by angles 2i and 2i + 1.
+__device__ __forceinline__ void turn(const Angles& t, int i, float& x0, float& x1, float& y0, float& y1) {
+  const Two x(x0, x1), y(y0, y1);
+  fma(x, t.c[i], mul(y, t.n[i])).get(x0, x1);
+  fma(y, t.c[i], mul(x, t.s[i])).get(y0, y1);
+}
 // Rotates across two chunks (halves of the rotated dims), or the pairs within one (interleaved).
-__device__ __forceinline__ void rotate_across(float (&x)[8], float (&y)[8], const float (&s)[8], const float (&c)[8]) {
+__device__ __forceinline__ void rotate_across(float (&x)[8], float (&y)[8], const Angles& t) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float a0 = x[i], a1 = y[i];
-    x[i] = a0 * c[i] - a1 * s[i];
-    y[i] = a1 * c[i] + a0 * s[i];
-  }
+  for (int i = 0; i < 4; ++i) turn(t, i, x[2 * i], x[2 * i + 1], y[2 * i], y[2 * i + 1]);
 }
 template <int AT>
-__device__ __forceinline__ void rotate_within(float (&x)[8], const float (&s)[8], const float (&c)[8]) {
+__device__ __forceinline__ void rotate_within(float (&x)[8], const Angles& t) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a0 = x[2 * i], a1 = x[2 * i + 1];
-    x[2 * i] = a0 * c[AT + i] - a1 * s[AT + i];
-    x[2 * i + 1] = a1 * c[AT + i] + a0 * s[AT + i];
-  }
+  for (int i = 0; i < 2; ++i) turn(t, AT / 2 + i, x[4 * i], x[4 * i + 2], x[4 * i + 1], x[4 * i + 3]);
 }
 
 __device__ __forceinline__ int unit_of(const Kv8AppendArgs& a, int b) { return __ldg(a.cu + b) / kBlock + 2 * b; }
@@ -485,20 +508,26 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
     ++next;
     asm volatile("cp.async.commit_group;" ::: "memory");
   };
-  float s[8], c[8];
+  Angles angles;
   auto rotate = [&](float (&x0)[8], float (&x1)[8]) {
-    if (across) rotate_across(x0, x1, s, c);
-    if (within0) rotate_within<0>(x0, s, c);
-    if (within1) rotate_within<4>(x1, s, c);
+    if (across) rotate_across(x0, x1, angles);
+    if (within0) rotate_within<0>(x0, angles);
+    if (within1) rotate_within<4>(x1, angles);
   };
   if (in) {
 #pragma unroll
     for (int i = 0; i < kAhead - 1; ++i) copy_next(i);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; i += 2) {
       if (!(across || (i < 4 ? within0 : within1))) continue;
       const int pair = across ? c0 + i : i < 4 ? c0 / 2 + i : c1 / 2 + i - 4;
-      sin_cos<T>(turn_fraction(__ldg(a.inv_freq + pair)), first + r, s[i], c[i]);
+      const float2 f = __ldg(reinterpret_cast<const float2*>(a.inv_freq + pair));
+      float s0, c0_, s1, c1_;
+      sin_cos<T>(turn_fraction(f.x), first + r, s0, c0_);
+      sin_cos<T>(turn_fraction(f.y), first + r, s1, c1_);
+      angles.s[i / 2] = Two(s0, s1);
+      angles.n[i / 2] = Two(-s0, -s1);
+      angles.c[i / 2] = Two(c0_, c1_);
     }
     // queries
     T* out = (T*)a.q_out + (token * a.Hq + y) * hd;
@@ -522,13 +551,22 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
 
   // keys and values
   int ks = 0;  // slot of the key
+  uint8_t* head[2];
+  float* scale[2];
+  if (n_kv > 0) {
+    const size_t at = (size_t)page * a.page_stride + (size_t)y * kBlock * hd, sc = (size_t)page * a.Hkv + y;
+    head[0] = a.kc + at;
+    head[1] = a.vc + at;
+    scale[0] = a.ks + sc;
+    scale[1] = a.vs + sc;
+  }
+  const unsigned row = (unsigned)(slot0 + r) * hd;
   for (int j = 0; j < n_kv; ++j) {
-    const int h = y + j * ny, parity = j & 1, vs = ks + 1 < kAhead ? ks + 1 : 0;
-    const size_t sc = (size_t)page * a.Hkv + h;
+    const int parity = j & 1, vs = ks + 1 < kAhead ? ks + 1 : 0;
     float held[2] = {0.f, 0.f};
     if (slot0 > 0) {
-      held[0] = a.ks[sc];
-      held[1] = a.vs[sc];
+      held[0] = *scale[0];
+      held[1] = *scale[1];
     }
     asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 3) : "memory");  // both items
     float kx[2][8] = {};
@@ -574,22 +612,20 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
       largest(top[parity], true);
     }
     const float now[2] = {fmaxf(held[0], pow2(scale_exp(mk))), fmaxf(held[1], pow2(scale_exp(mv)))};
-    uint8_t* const head[2] = {a.kc + (size_t)page * a.page_stride + (size_t)h * kBlock * hd,
-                              a.vc + (size_t)page * a.page_stride + (size_t)h * kBlock * hd};
+    if (slot0 > 0) {
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      if (slot0 > 0 && now[e] > held[e]) {  // the codes held before move to the new scale
+      for (int e = 0; e < 2; ++e) {
+        if (!(now[e] > held[e])) continue;  // the codes held before move to the new scale
         const float ratio = held[e] / now[e];
         for (int i = tid; i < slot0 * hd / 4; i += blockDim.x) {
           uint32_t* w = reinterpret_cast<uint32_t*>(head[e]) + i;
           *w = rescale4(*w, ratio);
         }
       }
-      if (tid == e) (e ? a.vs : a.ks)[sc] = now[e];
     }
+    if (tid < 2) *(tid ? scale[1] : scale[0]) = tid ? now[1] : now[0];
     if (in) {
-      const float ik = 1.f / now[0], iv = 1.f / now[1];
-      const size_t off = (size_t)(slot0 + r) * hd;
+      const float ik = __frcp_rn(now[0]), iv = __frcp_rn(now[1]);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (x && !two) break;
@@ -603,8 +639,8 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
             kx[x][i] = or_nan(kx[x][i]);
           }
         }
-        *reinterpret_cast<uint2*>(head[0] + off + at) = codes8(kx[x], ik);
-        *reinterpret_cast<uint2*>(head[1] + off + at) = codes8(v, iv);
+        *reinterpret_cast<uint2*>(head[0] + row + at) = codes8(kx[x], ik);
+        *reinterpret_cast<uint2*>(head[1] + row + at) = codes8(v, iv);
       }
     }
     if (in) {
@@ -612,6 +648,11 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
       copy_next(ks);
     }
     ks = vs + 1 < kAhead ? vs + 1 : 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      head[e] += step * kBlock;
+      scale[e] += ny;
+    }
   }
   asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
