@@ -292,23 +292,6 @@ __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-// Two fp32 operations in one instruction.
-struct Two {
-  uint64_t v;
-  __device__ __forceinline__ Two() {}
-  __device__ __forceinline__ Two(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
-  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
-};
-__device__ __forceinline__ Two mul(Two a, Two b) {
-  Two r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
-  return r;
-}
-__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
-  Two r;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
-  return r;
-}
 __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {  // numbers or NaN, no infinities
   uint2 u;
   const Two f(inv, inv);
@@ -658,7 +641,7 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
 }
 
 template <typename T>
-cudaError_t launch_append(const Kv8AppendArgs& a, int sm_count, cudaStream_t st) {
+cudaError_t launch_append(const Kv8AppendArgs& a, cudaStream_t st) {
   if (!a.cu) {
     const long long warps = (long long)a.B * (a.Hkv + a.Hq);
     const unsigned grid = (unsigned)((warps + kOneWarps - 1) / kOneWarps) + 1;
@@ -667,22 +650,11 @@ cudaError_t launch_append(const Kv8AppendArgs& a, int sm_count, cudaStream_t st)
     return cudaGetLastError();
   }
   const int threads = kBlock * ((a.hd + 15) / 16);
-  const int units = a.n_tokens / kBlock + 2 * a.B, pages = a.n_tokens / kBlock + a.B;
+  const int units = a.n_tokens / kBlock + 2 * a.B;
   const int smem = ahead<T>() * 2 * 8 * (int)sizeof(T) * threads;
-  // Heads are shared out among ny CTAs: more of them fill the machine evenly, but each finds the angles
-  // again, which costs about as much as kAngles rows. A page for each sequence's end is counted.
-  constexpr float kAngles = 6.f;
-  const int per_sm = std::max(1, std::min(1024 / threads, 220 * 1024 / smem)), heads = a.Hq + 2 * a.Hkv;
-  int ny = 1;
-  float best = 0.f;
-  for (int y = 1; y <= a.Hkv && y <= 64; ++y) {
-    const long long waves = ((long long)pages * y + (long long)per_sm * sm_count - 1) / ((long long)per_sm * sm_count);
-    const float cost = (float)waves * (kAngles + (float)((heads + y - 1) / y));
-    if (y == 1 || cost < best) {
-      best = cost;
-      ny = y;
-    }
-  }
+  // Heads are shared out among up to 8 CTAs. Each finds the page's angles again, but they fill the machine
+  // evenly to the end: 121 us for 32K tokens of 32 + 8 heads with 8 of them, 126 with 4, 132 with one.
+  const int ny = std::min(a.Hkv, 8);
   void (*kernel)(Kv8AppendArgs, int) = kv8_append_kernel<T, Turn::kMixed>;
   if (a.hd % 16 == 0 && a.rot == 0) kernel = kv8_append_kernel<T, Turn::kNone>;
   else if (a.hd % 16 == 0 && a.rot == a.hd)
@@ -697,9 +669,9 @@ cudaError_t launch_append(const Kv8AppendArgs& a, int sm_count, cudaStream_t st)
 }  // namespace
 }  // namespace kv8
 
-cudaError_t launch_kv8_append(const Kv8AppendArgs& a, lr_dtype dt, int sm_count, cudaStream_t st) {
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, lr_dtype dt, cudaStream_t st) {
   if (a.B == 0) return cudaMemsetAsync(a.err, 0, 256, st);
-  return dt == LR_BF16 ? kv8::launch_append<__nv_bfloat16>(a, sm_count, st) : kv8::launch_append<float>(a, sm_count, st);
+  return dt == LR_BF16 ? kv8::launch_append<__nv_bfloat16>(a, st) : kv8::launch_append<float>(a, st);
 }
 
 }  // namespace lr

@@ -1,11 +1,16 @@
 // Decode attention over the 8-bit paged cache: the choice of the kernel, and the kernel on the CUDA
 // cores for every storage type, head_dim and group size the entry point takes.
 //
-// One CTA of 128 threads walks its share of the batch's tiles (kv8_common.cuh), two pages of 64
-// tokens at a time: thread t holds the score of token t for the G query heads of the KV head
-// (q.k over the codes, times the page's key scale), the running maximum of the online softmax
-// moves, and then thread d sums p v over the tokens for column d. Everything is fp32. Bound by
-// its own instructions (a conversion and G multiply-adds per cached number).
+// One CTA of 128 threads walks its share of the batch's tiles (kv8_common.cuh). Warp w takes the 32 tokens from
+// 32 w on of every tile, by itself: its own maximum, sum and accumulators, joined with the other warps' at the
+// segment's end. A row is read by kLanes lanes, 16 bytes (8 for more than four query heads) each, so a lane has
+// kDims dims of q of every query head in registers, and of the accumulators. Scores are summed across the lanes
+// by exchanging heads, so each lane ends up with one head's; the weights go through shared memory to the lanes
+// that need all heads'. Values of a batch and the keys of the next are on their way while scores and
+// weights are worked out.
+//
+// Everything is fp32, two multiply-adds to an instruction. Bound by its instructions: about one per 7 bytes
+// with four query heads.
 #include <algorithm>
 
 #include "kv8_common.cuh"
@@ -14,187 +19,271 @@ namespace lr {
 namespace kv8 {
 namespace {
 
-constexpr int NT = kTileTokens;
-static_assert(NT == 128, "thread t owns token t of a tile");
+constexpr int NT = 128, kWarps = NT / 32;
+static_assert(kTileTokens == NT, "32 tokens of a tile to a warp");
 
-// Eight codes as fp32.
-__device__ __forceinline__ void codes8(uint2 u, float (&v)[8]) {
-  float2 f;
-  f = e4m3x2_value(u.x & 0xffffu); v[0] = f.x; v[1] = f.y;
-  f = e4m3x2_value(u.x >> 16);     v[2] = f.x; v[3] = f.y;
-  f = e4m3x2_value(u.y & 0xffffu); v[4] = f.x; v[5] = f.y;
-  f = e4m3x2_value(u.y >> 16);     v[6] = f.x; v[7] = f.y;
+// MG: query heads the registers hold; kLanes: lanes that share a row (head_dim <= kLanes * kDims).
+template <int MG, int kLanes>
+struct Shape {
+  static constexpr int kDims = 64 / MG;
+  static constexpr int kTokens = 32 / kLanes;                                    // of a step
+  static constexpr int kSteps = kLanes < 128 / kDims ? kLanes : 128 / kDims;     // of a batch: 128 bytes a lane at most
+  static constexpr int kBatch = kSteps * kTokens, kBatches = 32 / kBatch;
+  static constexpr int kWords = kDims / 4;
+};
+
+// This lane's part of a row: `n` bytes of it (a multiple of 8) are there, the rest is 0.
+template <int kWords>
+__device__ __forceinline__ void load_row(const uint8_t* at, int n, bool wide, uint32_t (&w)[kWords]) {
+#pragma unroll
+  for (int i = 0; i < kWords; ++i) w[i] = 0;
+  if (kWords == 4 && wide && n >= 16) {
+    const uint4 v = __ldg(reinterpret_cast<const uint4*>(at));
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
+    return;
+  }
+#pragma unroll
+  for (int i = 0; i < kWords; i += 2)
+    if (n > 4 * i) {
+      const uint2 v = __ldg(reinterpret_cast<const uint2*>(at + 4 * i));
+      w[i] = v.x;
+      w[i + 1] = v.y;
+    }
+}
+__device__ __forceinline__ Two code_pair(uint32_t codes) {
+  const float2 v = e4m3x2_value(codes & 0xffffu);
+  return Two(v.x, v.y);
 }
 
-template <typename T, int MD>  // MD: columns of a thread (head_dim <= 128 MD)
-__global__ void __launch_bounds__(NT) kv8_attn_kernel(Kv8AttnArgs a) {
+template <int MG, int kLanes>
+__global__ void __launch_bounds__(NT, 2) kv8_attn_kernel(Kv8AttnArgs a, bool bf16) {
+  using S = Shape<MG, kLanes>;
   __shared__ long long scratch[NT + 4];
-  __shared__ __align__(16) float qs[256][8];   // q * scale, head fastest
-  __shared__ __align__(16) float ps[NT][8];    // p * value scale of the tile's tokens
-  __shared__ float red[4][8];
+  __shared__ __align__(16) float ps[kWarps][S::kBatch][MG];  // weight times value scale
+  __shared__ __align__(16) float olds[kWarps][MG];
+  __shared__ float ml[kWarps][2][MG];
+  __shared__ __align__(16) float sums[kWarps][MG][256];
   __shared__ int err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int hd = a.hd, G = a.G;
+  const int part = lane % kLanes, tg = lane / kLanes, d0 = part * S::kDims;
+  const int n_dims = max(0, min(S::kDims, hd - d0));
+  const bool wide = hd % 16 == 0;
+  // the head whose scores this lane ends up with
+  const int my_g = (part & 1) * (MG / 2) + ((part >> 1) & 1) * (MG / 4) + (MG == 8 ? (part >> 2) & 1 : 0);
   if (tid == 0) err = 0;
   grid_dependency();
   Walk k(a, find_work<NT>(a, scratch));
+  auto number = [&](const void* p, size_t i) {
+    return bf16 ? to_f32(((const __nv_bfloat16*)p)[i]) : ((const float*)p)[i];
+  };
   while (k.next()) {
     const int* table = a.table + (size_t)k.b * a.max_pages;
     const size_t row0 = ((size_t)k.b * a.Hkv + k.h) * G;
-    __syncthreads();
-    for (int i = tid; i < 8 * hd; i += NT) {
-      const int g = i / hd, d = i % hd;
-      qs[d][g] = g < G ? to_f32(((const T*)a.q)[(row0 + g) * hd + d]) * a.scale : 0.f;
-    }
-    __syncthreads();
-    float m[8], l[8], acc[MD][8];
+    Two q[MG][S::kDims / 2];
 #pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      m[g] = -CUDART_INF_F;
-      l[g] = 0.f;
+    for (int g = 0; g < MG; ++g)
 #pragma unroll
-      for (int x = 0; x < MD; ++x) acc[x][g] = 0.f;
-    }
-    for (int i = k.tile0; i < k.tile1; ++i) {
-      const int p0 = k.sp.page0 + i * kTilePages;  // pages p0, p0 + 1 of the sequence
-      const int t = p0 * kBlock + tid;
-      int id[kTilePages];
-#pragma unroll
-      for (int x = 0; x < kTilePages; ++x) {
-        id[x] = -1;
-        if ((p0 + x) * kBlock < k.sp.n) {
-          id[x] = __ldg(table + p0 + x);
-          if ((unsigned)id[x] >= (unsigned)a.n_pages) {
-            id[x] = -1;
-            if (tid == 0) err |= LR_DEVERR_PAGE;
-          }
-        }
+      for (int d = 0; d < S::kDims; d += 2) {
+        const bool there = g < G && d < n_dims;
+        const size_t at = (row0 + g) * hd + d0 + d;
+        q[g][d / 2] = there ? Two(number(a.q, at) * a.scale, number(a.q, at + 1) * a.scale) : Two(0.f, 0.f);
       }
-      const int pg = tid < kBlock ? id[0] : id[1];
-      const bool seen = t >= k.sp.lo && t < k.sp.n && pg >= 0;
-      float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      float vs = 0.f;
-      if (seen) {
-        const uint8_t* row = a.kc + (size_t)pg * a.page_stride + ((size_t)k.h * kBlock + (tid & (kBlock - 1))) * hd;
-        for (int d = 0; d < hd; d += 8) {
-          float kv[8];
-          codes8(__ldg(reinterpret_cast<const uint2*>(row + d)), kv);
+    Two acc[MG][S::kDims / 2];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float4 q0 = *reinterpret_cast<const float4*>(&qs[d + e][0]);
-            s[0] = fmaf(kv[e], q0.x, s[0]);
-            s[1] = fmaf(kv[e], q0.y, s[1]);
-            s[2] = fmaf(kv[e], q0.z, s[2]);
-            s[3] = fmaf(kv[e], q0.w, s[3]);
-            if (G > 4) {
-              const float4 q1 = *reinterpret_cast<const float4*>(&qs[d + e][4]);
-              s[4] = fmaf(kv[e], q1.x, s[4]);
-              s[5] = fmaf(kv[e], q1.y, s[5]);
-              s[6] = fmaf(kv[e], q1.z, s[6]);
-              s[7] = fmaf(kv[e], q1.w, s[7]);
-            }
-          }
-        }
-        const float ks = __ldg(a.ks + (size_t)pg * a.Hkv + k.h);
-        vs = __ldg(a.vs + (size_t)pg * a.Hkv + k.h);
+    for (int g = 0; g < MG; ++g)
 #pragma unroll
-        for (int g = 0; g < 8; ++g) s[g] *= ks;
-      }
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        if (!seen) s[g] = -CUDART_INF_F;
-        const float top = warp_max(s[g]);
-        if (lane == 0) red[warp][g] = top;
-      }
-      __syncthreads();
-      float old[8];
-#pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        const float top = fmaxf(fmaxf(fmaxf(red[0][g], red[1][g]), fmaxf(red[2][g], red[3][g])), m[g]);
-        const float ref = top == -CUDART_INF_F ? 0.f : top;
-        old[g] = exp2f(m[g] - ref);
-        const float p = exp2f(s[g] - ref);
-        l[g] = fmaf(l[g], old[g], p);
-        ps[tid][g] = seen ? p * vs : 0.f;
-        m[g] = top;
-      }
-      __syncthreads();
-      // rows [r0, r1) of the tile are attended; rows of pages that are left out are not read
-      const int r0 = max(0, k.sp.lo - p0 * kBlock), r1 = min(kTileTokens, k.sp.n - p0 * kBlock);
-#pragma unroll
-      for (int x = 0; x < MD; ++x) {
-        const int d = tid + x * NT;
-        if (d < hd) {
-#pragma unroll
-          for (int g = 0; g < 8; ++g) acc[x][g] *= old[g];
-#pragma unroll
-          for (int half = 0; half < kTilePages; ++half) {
-            if (id[half] < 0) continue;
-            const uint8_t* col = a.vc + (size_t)id[half] * a.page_stride + (size_t)k.h * kBlock * hd + d;
-            const int b0 = half * kBlock;
-#pragma unroll 8
-            for (int r = max(r0, b0); r < min(r1, b0 + kBlock); ++r) {
-              const float v = e4m3x2_value(__ldg(col + (size_t)(r - b0) * hd)).x;
-              const float4 w0 = *reinterpret_cast<const float4*>(&ps[r][0]);
-              acc[x][0] = fmaf(w0.x, v, acc[x][0]);
-              acc[x][1] = fmaf(w0.y, v, acc[x][1]);
-              acc[x][2] = fmaf(w0.z, v, acc[x][2]);
-              acc[x][3] = fmaf(w0.w, v, acc[x][3]);
-              if (G > 4) {
-                const float4 w1 = *reinterpret_cast<const float4*>(&ps[r][4]);
-                acc[x][4] = fmaf(w1.x, v, acc[x][4]);
-                acc[x][5] = fmaf(w1.y, v, acc[x][5]);
-                acc[x][6] = fmaf(w1.z, v, acc[x][6]);
-                acc[x][7] = fmaf(w1.w, v, acc[x][7]);
-              }
-            }
-          }
-        }
-      }
-    }
-    // the sums of p are spread over the threads
-    __syncthreads();
-#pragma unroll
-    for (int g = 0; g < 8; ++g) {
-      const float x = warp_sum(l[g]);
-      if (lane == 0) red[warp][g] = x;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int g = 0; g < 8; ++g) l[g] = (red[0][g] + red[1][g]) + (red[2][g] + red[3][g]);
+      for (int d = 0; d < S::kDims / 2; ++d) acc[g][d] = Two(0.f, 0.f);
+    float m = -CUDART_INF_F, l = 0.f;  // of head my_g
 
-    if (!k.whole()) {
-      float* slot = a.part + (size_t)piece_slot(k.wk, k.seg_first) * a.part_stride;
+    // batch i of the range is batch i % kBatches of the warp's tokens of tile tile0 + i / kBatches
+    const int n_batches = (k.tile1 - k.tile0) * S::kBatches;
+    auto first_token = [&](int i) {
+      return (k.sp.page0 + (k.tile0 + i / S::kBatches) * kTilePages) * kBlock + warp * 32 + i % S::kBatches * S::kBatch;
+    };
+    auto page_of = [&](int i) {  // page of a batch, -1: none
+      if (i >= n_batches) return -1;
+      const int p = first_token(i) / kBlock;
+      if (p * kBlock >= k.sp.n) return -1;
+      int id = __ldg(table + p);
+      if ((unsigned)id >= (unsigned)a.n_pages) {
+        if (lane == 0) atomicOr(&err, LR_DEVERR_PAGE);
+        id = -1;
+      }
+      return id;
+    };
+    auto seen = [&](int i, int step) {
+      const int t = first_token(i) + step * S::kTokens + tg;
+      return t >= k.sp.lo && t < k.sp.n;
+    };
+    auto load = [&](const uint8_t* codes, int i, int id, uint32_t (&w)[S::kSteps][S::kWords]) {
+      const uint8_t* head = codes + (size_t)max(id, 0) * a.page_stride + (size_t)k.h * kBlock * hd;
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        if (g >= G) break;
+      for (int s = 0; s < S::kSteps; ++s) {
+        const int r = (first_token(i) + s * S::kTokens + tg) % kBlock;
+        load_row(head + (unsigned)(r * hd + d0), id >= 0 && seen(i, s) ? n_dims : 0, wide, w[s]);
+      }
+    };
+    int id = page_of(0), id_next = page_of(1);
+    uint32_t kw[S::kSteps][S::kWords], vw[S::kSteps][S::kWords];
+    load(a.kc, 0, id, kw);
+    for (int i = 0; i < n_batches; ++i) {
+      load(a.vc, i, id, vw);
+      float ks = 0.f, vs = 0.f;
+      if (id >= 0) {
+        ks = __ldg(a.ks + (size_t)id * a.Hkv + k.h);
+        vs = __ldg(a.vs + (size_t)id * a.Hkv + k.h);
+      }
+      float x[S::kSteps];
 #pragma unroll
-        for (int x = 0; x < MD; ++x)
-          if (tid + x * NT < hd) slot[g * hd + tid + x * NT] = acc[x][g];
-        if (tid == 0) {
-          slot[G * hd + g] = m[g];
-          slot[G * hd + 8 + g] = l[g];
+      for (int s = 0; s < S::kSteps; ++s) {
+        Two dot[MG];
+#pragma unroll
+        for (int g = 0; g < MG; ++g) dot[g] = Two(0.f, 0.f);
+#pragma unroll
+        for (int d = 0; d < S::kDims / 2; ++d) {
+          const Two v = code_pair(kw[s][d / 2] >> (d % 2 * 16));
+#pragma unroll
+          for (int g = 0; g < MG; ++g) dot[g] = fma(v, q[g][d], dot[g]);
+        }
+        float v[MG];
+#pragma unroll
+        for (int g = 0; g < MG; ++g) {
+          float lo, hi;
+          dot[g].get(lo, hi);
+          v[g] = lo + hi;
+        }
+#pragma unroll
+        for (int off = 1, n = MG; off < kLanes; off *= 2) {
+          if (n > 1) {  // this lane keeps half of the heads and gives the other half away
+            n /= 2;
+            const bool upper = part & off;
+#pragma unroll
+            for (int g = 0; g < n; ++g) {
+              const float give = upper ? v[g] : v[n + g], keep = upper ? v[n + g] : v[g];
+              v[g] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+            }
+          } else {
+            v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
+          }
+        }
+        x[s] = id >= 0 && seen(i, s) ? v[0] * ks : -CUDART_INF_F;
+      }
+      load(a.kc, i + 1, id_next, kw);
+      const int id_after = page_of(i + 2);
+
+      float top = x[0];
+#pragma unroll
+      for (int s = 1; s < S::kSteps; ++s) top = fmaxf(top, x[s]);
+#pragma unroll
+      for (int off = kLanes; off < 32; off *= 2) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      top = fmaxf(top, m);
+      const float ref = top == -CUDART_INF_F ? 0.f : top, old = exp2f(m - ref);
+      m = top;
+      l *= old;
+      __syncwarp();  // the last batch's weights have been read
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s) {
+        const float p = exp2f(x[s] - ref);
+        l += p;
+        if (part < MG) ps[warp][s * S::kTokens + tg][my_g] = x[s] == -CUDART_INF_F ? 0.f : p * vs;
+      }
+      if (part < MG && tg == 0) olds[warp][my_g] = old;
+      __syncwarp();
+#pragma unroll
+      for (int g = 0; g < MG; ++g) {
+        const Two f(olds[warp][g], olds[warp][g]);
+#pragma unroll
+        for (int d = 0; d < S::kDims / 2; ++d) acc[g][d] = mul(acc[g][d], f);
+      }
+#pragma unroll
+      for (int s = 0; s < S::kSteps; ++s) {
+        Two w[MG];
+#pragma unroll
+        for (int g = 0; g < MG; g += 4) {
+          const float4 f = *reinterpret_cast<const float4*>(&ps[warp][s * S::kTokens + tg][g]);
+          w[g] = Two(f.x, f.x);
+          w[g + 1] = Two(f.y, f.y);
+          w[g + 2] = Two(f.z, f.z);
+          w[g + 3] = Two(f.w, f.w);
+        }
+#pragma unroll
+        for (int d = 0; d < S::kDims / 2; ++d) {
+          const Two v = code_pair(vw[s][d / 2] >> (d % 2 * 16));
+#pragma unroll
+          for (int g = 0; g < MG; ++g) acc[g][d] = fma(v, w[g], acc[g][d]);
         }
       }
-    } else {
-      Joined j[8];
+      id = id_next;
+      id_next = id_after;
+    }
+    // the token groups of the warp, then the warps
 #pragma unroll
-      for (int g = 0; g < 8; ++g)
-        if (g < G) j[g] = join_prev(a, row0 + g, m[g], l[g]);
-      __syncthreads();  // lse may be lse_prev: every thread has read it
+    for (int off = kLanes; off < 32; off *= 2) l += __shfl_xor_sync(0xffffffffu, l, off);
+    __syncthreads();
+    if (part < MG && tg == 0) {
+      ml[warp][0][my_g] = m;
+      ml[warp][1][my_g] = l;
+    }
 #pragma unroll
-      for (int g = 0; g < 8; ++g) {
-        if (g >= G) break;
+    for (int g = 0; g < MG; ++g)
 #pragma unroll
-        for (int x = 0; x < MD; ++x) {
-          const int d = tid + x * NT;
-          if (d < hd) ((T*)a.o)[(row0 + g) * hd + d] = joined_value<T>(a, row0 + g, d, j[g], acc[x][g]);
+      for (int d = 0; d < S::kDims / 2; ++d) {
+        float lo, hi;
+        acc[g][d].get(lo, hi);
+#pragma unroll
+        for (int off = kLanes; off < 32; off *= 2) {
+          lo += __shfl_xor_sync(0xffffffffu, lo, off);
+          hi += __shfl_xor_sync(0xffffffffu, hi, off);
         }
-        if (a.lse && tid == 0) a.lse[row0 + g] = j[g].lse;
+        if (tg == 0 && 2 * d < n_dims) {
+          sums[warp][g][d0 + 2 * d] = lo;
+          sums[warp][g][d0 + 2 * d + 1] = hi;
+        }
+      }
+    __syncthreads();
+    const bool whole = k.whole();
+    float* slot = whole ? nullptr : a.part + (size_t)piece_slot(k.wk, k.seg_first) * a.part_stride;
+    for (int g = 0; g < G; ++g) {
+      float top = -CUDART_INF_F;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][0][g]);
+      const float ref = top == -CUDART_INF_F ? 0.f : top;
+      float f[kWarps], sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        f[w] = exp2f(ml[w][0][g] - ref);
+        sum = fmaf(ml[w][1][g], f[w], sum);
+      }
+      Joined j;
+      if (whole) {
+        j = join_prev(a, row0 + g, top, sum);
+        __syncthreads();  // lse may be lse_prev: every thread has read it
+        if (a.lse && tid == 0) a.lse[row0 + g] = j.lse;
+      } else if (tid == 0) {
+        slot[G * hd + g] = top;
+        slot[G * hd + 8 + g] = sum;
+      }
+      for (int d = tid; d < hd; d += NT) {
+        float v = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) v = fmaf(sums[w][g][d], f[w], v);
+        if (!whole) slot[g * hd + d] = v;
+        else if (bf16) ((__nv_bfloat16*)a.o)[(row0 + g) * hd + d] = joined_value<__nv_bfloat16>(a, row0 + g, d, j, v);
+        else ((float*)a.o)[(row0 + g) * hd + d] = joined_value<float>(a, row0 + g, d, j, v);
       }
     }
   }
+  __syncthreads();
   if (tid == 0) a.cta_err[blockIdx.x] = err;
+}
+
+void (*attn_kernel(int G, int hd))(Kv8AttnArgs, bool) {
+  if (G <= 4) return hd <= 64 ? kv8_attn_kernel<4, 4> : hd <= 128 ? kv8_attn_kernel<4, 8> : kv8_attn_kernel<4, 16>;
+  return hd <= 64 ? kv8_attn_kernel<8, 8> : hd <= 128 ? kv8_attn_kernel<8, 16> : kv8_attn_kernel<8, 32>;
 }
 
 // ------------------------------------------------------------------ joining the pieces
@@ -321,7 +410,7 @@ cudaError_t launch_attn(const Kv8AttnArgs& a, const Kv8AttnPlan& plan, cudaStrea
     if (!kv8_page_map(&mk, a.kc, a) || !kv8_page_map(&mv, a.vc, a)) return cudaErrorInvalidValue;
     e = launch_attn_tc(a, mk, mv, st);
   } else {
-    e = launch_overlapped(a.hd <= 128 ? kv8_attn_kernel<T, 1> : kv8_attn_kernel<T, 2>, dim3(plan.n_cta), NT, 0, st, a);
+    e = launch_overlapped(attn_kernel(a.G, a.hd), dim3(plan.n_cta), NT, 0, st, a, sizeof(T) == 2);
   }
   if (e != cudaSuccess) return e;
   return launch_overlapped(kv8_join_kernel<T>, dim3(plan.n_cta, a.G), JT, 0, st, a);

@@ -34,6 +34,23 @@ __device__ __forceinline__ __half2 e4m3x2_half2(uint32_t codes) {
 }
 __device__ __forceinline__ float2 e4m3x2_value(uint32_t codes) { return __half22float2(e4m3x2_half2(codes)); }
 
+// Two fp32 operations in one instruction.
+struct Two {
+  uint64_t v;
+  __device__ __forceinline__ Two() {}
+  __device__ __forceinline__ Two(float lo, float hi) { asm("mov.b64 %0, {%1, %2};" : "=l"(v) : "f"(lo), "f"(hi)); }
+  __device__ __forceinline__ void get(float& lo, float& hi) const { asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v)); }
+};
+__device__ __forceinline__ Two mul(Two a, Two b) {
+  Two r;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+  return r;
+}
+__device__ __forceinline__ Two fma(Two a, Two b, Two c) {
+  Two r;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+  return r;
+}
 // Waits for the grid before in the stream, then lets the next one be launched: what that one reads before
 // its own wait was complete before this grid went on.
 __device__ __forceinline__ void grid_dependency() {
