@@ -475,41 +475,44 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
       vs1 = meta.vs[1];
     }
     if (!(meta.flags & LAST)) continue;
-    add_values(it);
-    // the sums of p are spread over the threads
     const size_t row0 = (size_t)meta.head * a.G + g0;
+    const bool whole = meta.flags & WHOLE;
+    float prev[kHeads];  // the earlier partial result, on its way while the last product ends
 #pragma unroll
-    for (int g = 0; g < kHeads; ++g) {
-      const float v = warp_sum(l[g]);
-      if (lane == 0) red[warp * 4 + g] = v;
-    }
+    for (int g = 0; g < kHeads; ++g)
+      prev[g] = whole && a.o_prev && g < G ? to_f32(((const __nv_bfloat16*)a.o_prev)[(row0 + g) * kHd + tid]) : 0.f;
+    // the sums of p are spread over the threads: exchanging heads, a lane ends up with one head's
+    const bool up1 = lane & 1, up2 = lane & 2;
+    float v0 = (up1 ? l[2] : l[0]) + __shfl_xor_sync(0xffffffffu, up1 ? l[0] : l[2], 1);
+    float v1 = (up1 ? l[3] : l[1]) + __shfl_xor_sync(0xffffffffu, up1 ? l[1] : l[3], 1);
+    float sum = (up2 ? v1 : v0) + __shfl_xor_sync(0xffffffffu, up2 ? v0 : v1, 2);
+#pragma unroll
+    for (int off = 4; off < 32; off *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    if (lane < kHeads) red[warp * 4 + (lane & 1) * 2 + (lane >> 1)] = sum;
+    add_values(it);
     soft_sync(group);
-#pragma unroll
-    for (int g = 0; g < kHeads; ++g) l[g] = (red[g] + red[4 + g]) + (red[8 + g] + red[12 + g]);
-
-    if (!(meta.flags & WHOLE)) {
+    const int mine = lane % kHeads;  // the head that this lane finishes
+    sum = (red[mine] + red[4 + mine]) + (red[8 + mine] + red[12 + mine]);
+    const float top = mine < 2 ? (mine == 0 ? m[0] : m[1]) : (mine == 2 ? m[2] : m[3]);
+    if (!whole) {
       float* slot = a.part + (size_t)meta.slot * a.part_stride;
 #pragma unroll
-      for (int g = 0; g < kHeads; ++g) {
-        if (g >= G) break;
-        slot[(g0 + g) * kHd + tid] = acc[g];
-        if (tid == 0) {
-          slot[a.G * kHd + g0 + g] = m[g];
-          slot[a.G * kHd + 8 + g0 + g] = l[g];
-        }
+      for (int g = 0; g < kHeads; ++g)
+        if (g < G) slot[(g0 + g) * kHd + tid] = acc[g];
+      if (tid < G) {
+        slot[a.G * kHd + g0 + tid] = top;
+        slot[a.G * kHd + 8 + g0 + tid] = sum;
       }
     } else {
-      Joined j[kHeads];
-#pragma unroll
-      for (int g = 0; g < kHeads; ++g)
-        if (g < G) j[g] = join_prev(a, row0 + g, m[g], l[g]);
-      soft_sync(group);  // lse may be lse_prev: every thread has read it
+      Joined j{0.f, 0.f, 0.f};
+      if (mine < G) j = join_prev(a, row0 + mine, top, sum);
+      if (a.lse_prev) soft_sync(group);  // it may be lse: every warp has read it
 #pragma unroll
       for (int g = 0; g < kHeads; ++g) {
-        if (g >= G) break;
-        ((__nv_bfloat16*)a.o)[(row0 + g) * kHd + tid] = joined_value<__nv_bfloat16>(a, row0 + g, tid, j[g], acc[g]);
-        if (a.lse && tid == 0) a.lse[row0 + g] = j[g].lse;
+        const float inv = __shfl_sync(0xffffffffu, j.inv, g), w = __shfl_sync(0xffffffffu, j.w_prev, g);
+        if (g < G) ((__nv_bfloat16*)a.o)[(row0 + g) * kHd + tid] = from_f32<__nv_bfloat16>(join_value(acc[g], inv, prev[g], w));
       }
+      if (a.lse && tid < G) a.lse[row0 + tid] = j.lse;
     }
   }
 }

@@ -254,15 +254,19 @@ __device__ __forceinline__ Joined join_prev(const Kv8AttnArgs& a, size_t row, fl
   const float wp = lp == -CUDART_INF_F ? 0.f : exp2f(lp - top);
   const float sum = fmaf(l, w, wp);
   j.inv = w / sum;
-  j.w_prev = wp / sum;  // NaN where the sum is: o_prev may be null all the same
+  j.w_prev = wp / sum;  // NaN where the sum is, with or without an earlier part
   j.lse = kLn2 * (top + log2f(sum));
   return j;
 }
+// acc * inv + prev * w; what a weight of 0 goes with is left out, whatever it is.
+__device__ __forceinline__ float join_value(float acc, float inv, float prev, float w) {
+  const float y = inv != 0.f ? acc * inv : 0.f;
+  return w != 0.f ? fmaf(prev, w, y) : y;
+}
 template <typename T>
 __device__ __forceinline__ T joined_value(const Kv8AttnArgs& a, size_t row, int d, const Joined& j, float acc) {
-  float y = j.inv != 0.f ? acc * j.inv : 0.f;
-  if (a.o_prev && j.w_prev != 0.f) y = fmaf(to_f32(((const T*)a.o_prev)[row * a.hd + d]), j.w_prev, y);
-  return from_f32<T>(y);
+  const float prev = a.o_prev ? to_f32(((const T*)a.o_prev)[row * a.hd + d]) : 0.f;
+  return from_f32<T>(join_value(acc, j.inv, prev, j.w_prev));
 }
 
 // ---- pieces of a split segment
