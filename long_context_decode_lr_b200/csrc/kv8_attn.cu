@@ -115,27 +115,50 @@ __global__ void __launch_bounds__(NT, 2) kv8_attn_kernel(Kv8AttnArgs a, bool bf1
       }
       return id;
     };
-    auto seen = [&](int i, int step) {
-      const int t = first_token(i) + step * S::kTokens + tg;
-      return t >= k.sp.lo && t < k.sp.n;
+    // the tokens of a batch that are attended, counted from its first: [from, to)
+    struct Part {
+      int id, from, to;
     };
-    auto load = [&](const uint8_t* codes, int i, int id, uint32_t (&w)[S::kSteps][S::kWords]) {
-      const uint8_t* head = codes + (size_t)max(id, 0) * a.page_stride + (size_t)k.h * kBlock * hd;
+    auto part_of = [&](int i) {
+      Part b{page_of(i), 0, 0};
+      if (b.id >= 0) {
+        const int t = first_token(i);
+        b.from = max(0, k.sp.lo - t);
+        b.to = min(S::kBatch, k.sp.n - t);
+      }
+      return b;
+    };
+    const unsigned step_bytes = S::kTokens * hd;
+    auto load = [&](const uint8_t* codes, int i, const Part& b, uint32_t (&w)[S::kSteps][S::kWords]) {
+      if (b.to <= b.from) {
 #pragma unroll
-      for (int s = 0; s < S::kSteps; ++s) {
-        const int r = (first_token(i) + s * S::kTokens + tg) % kBlock;
-        load_row(head + (unsigned)(r * hd + d0), id >= 0 && seen(i, s) ? n_dims : 0, wide, w[s]);
+        for (int s = 0; s < S::kSteps; ++s)
+#pragma unroll
+          for (int x = 0; x < S::kWords; ++x) w[s][x] = 0;
+        return;
+      }
+      const uint8_t* at = codes + (size_t)b.id * a.page_stride + (size_t)k.h * kBlock * hd +
+                          (unsigned)((first_token(i) % kBlock + tg) * hd + d0);
+      if (b.from == 0 && b.to == S::kBatch) {
+#pragma unroll
+        for (int s = 0; s < S::kSteps; ++s) load_row(at + s * step_bytes, n_dims, wide, w[s]);
+      } else {
+#pragma unroll
+        for (int s = 0; s < S::kSteps; ++s) {
+          const int t = s * S::kTokens + tg;
+          load_row(at + s * step_bytes, t >= b.from && t < b.to ? n_dims : 0, wide, w[s]);
+        }
       }
     };
-    int id = page_of(0), id_next = page_of(1);
+    Part now = part_of(0), next = part_of(1);
     uint32_t kw[S::kSteps][S::kWords], vw[S::kSteps][S::kWords];
-    load(a.kc, 0, id, kw);
+    load(a.kc, 0, now, kw);
     for (int i = 0; i < n_batches; ++i) {
-      load(a.vc, i, id, vw);
+      load(a.vc, i, now, vw);
       float ks = 0.f, vs = 0.f;
-      if (id >= 0) {
-        ks = __ldg(a.ks + (size_t)id * a.Hkv + k.h);
-        vs = __ldg(a.vs + (size_t)id * a.Hkv + k.h);
+      if (now.id >= 0) {
+        ks = __ldg(a.ks + (size_t)now.id * a.Hkv + k.h);
+        vs = __ldg(a.vs + (size_t)now.id * a.Hkv + k.h);
       }
       float x[S::kSteps];
 #pragma unroll
@@ -170,10 +193,17 @@ __global__ void __launch_bounds__(NT, 2) kv8_attn_kernel(Kv8AttnArgs a, bool bf1
             v[0] += __shfl_xor_sync(0xffffffffu, v[0], off);
           }
         }
-        x[s] = id >= 0 && seen(i, s) ? v[0] * ks : -CUDART_INF_F;
+        x[s] = v[0] * ks;
       }
-      load(a.kc, i + 1, id_next, kw);
-      const int id_after = page_of(i + 2);
+      if (now.from > 0 || now.to < S::kBatch) {
+#pragma unroll
+        for (int s = 0; s < S::kSteps; ++s) {
+          const int t = s * S::kTokens + tg;
+          if (t < now.from || t >= now.to) x[s] = -CUDART_INF_F;
+        }
+      }
+      load(a.kc, i + 1, next, kw);
+      const Part after = part_of(i + 2);
 
       float top = x[0];
 #pragma unroll
@@ -217,8 +247,8 @@ __global__ void __launch_bounds__(NT, 2) kv8_attn_kernel(Kv8AttnArgs a, bool bf1
           for (int g = 0; g < MG; ++g) acc[g][d] = fma(v, w[g], acc[g][d]);
         }
       }
-      id = id_next;
-      id_next = id_after;
+      now = next;
+      next = after;
     }
     // the token groups of the warp, then the warps
 #pragma unroll
