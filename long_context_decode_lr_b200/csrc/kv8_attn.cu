@@ -8,14 +8,14 @@
 // and row h + 8, which the same lanes hold, so
 //   S = Q K^T   (16 x 8 tokens): lane 4h + c has both terms of head h for tokens 2c and 2c + 1, and so
 //   O = P V     (16 x 8 dims) takes the weights from the registers that the scores were in.
-// The order of the dims is free: in S, lane 4t + c reads a quarter of token t's row, in O, lane 4d + c an eighth
-// of the rows of its four tokens. Everything else is fp32.
+// The order of the dims is free: in S, lane 4t + c reads every fourth 16 bytes of token t's row, in O, lane 4d + c
+// an eighth of the rows of its four tokens. Everything else is fp32.
 //
 // One CTA of 128 threads walks its share of the batch's tiles (kv8_common.cuh). Warp w takes the 32 tokens from
 // 32 w on of every tile, by itself: its own maximum, sum and accumulators, joined with the other warps' at the
-// segment's end. The values of a tile and the keys of the next are on their way while the scores are
-// worked out. Bound by HBM latency and by the conversions; on the CUDA cores, with two
-// multiply-adds to an instruction, it was bound by instructions at a third of HBM's rate.
+// segment's end. Every lane copies what it will use itself to shared memory, two tiles ahead (cp.async), so a
+// warp waits for nobody. Bound by the bytes under way; on the CUDA cores, with two multiply-adds to
+// an instruction, it was bound by instructions at a third of HBM's rate.
 #include <algorithm>
 
 #include "kv8_common.cuh"
@@ -43,63 +43,141 @@ __device__ __forceinline__ void split(float x, float y, uint32_t& t0, uint32_t& 
   t1 = bits(__floats2half2_rn((x - f.x) * 2048.f, (y - f.y) * 2048.f));
 }
 
-// This lane's part of a row: `n` bytes of it (a multiple of 8) are there, the rest is 0.
-template <int kWords>
-__device__ __forceinline__ void load_row(const uint8_t* at, int n, bool wide, uint32_t* w) {
-#pragma unroll
-  for (int i = 0; i < kWords; i += 4) {
-    if (kWords >= 4 && wide && n >= 4 * i + 16) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(at + 4 * i));
-      w[i] = v.x;
-      w[i + 1] = v.y;
-      w[i + 2] = v.z;
-      w[i + 3] = v.w;
-      continue;
-    }
-#pragma unroll
-    for (int x = i; x < i + 4 && x < kWords; x += 2) {
-      uint2 v = make_uint2(0u, 0u);
-      if (n > 4 * x) v = __ldg(reinterpret_cast<const uint2*>(at + 4 * x));
-      w[x] = v.x;
-      w[x + 1] = v.y;
-    }
+// Copies kBytes (8 or 16) of which `n` are there; the rest becomes 0. `wide`: 16-byte aligned.
+template <int kBytes>
+__device__ __forceinline__ void copy_part(uint32_t smem, const uint8_t* from, int n, bool wide) {
+  if (kBytes == 16 && wide) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(from), "r"(n) : "memory");
+    return;
   }
+#pragma unroll
+  for (int x = 0; x < kBytes; x += 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem + x), "l"(n > x ? from + x : from), "r"(n > x ? 8 : 0)
+                 : "memory");
+}
+__device__ __forceinline__ uint4 load16(uint32_t smem) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint2 load8(uint32_t smem) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(smem) : "memory");
+  return v;
 }
 
-// CTAs on an SM: what the registers allow.
-constexpr int resident(int hd) { return hd <= 64 ? 4 : 2; }
+template <int HD>
+struct Ring {
+  static constexpr int kStages = 3;
+  static constexpr int kBatch = HD <= 128 ? 32 : 16;      // tokens of a stage
+  static constexpr int kKeyParts = HD / 64;               // 16 bytes each, of a lane's quarter of a row
+  static constexpr int kValueBytes = HD == 64 ? 8 : 16;   // of a part of a lane's eighth of a row
+  static constexpr int kValueParts = HD / 8 / kValueBytes;
+  static constexpr int kValues = kBatch * HD;             // offset of the values in a stage
+  static constexpr int kStageBytes = 2 * kBatch * HD;
+  static constexpr int kWarpBytes = kStages * kStageBytes;
+  static constexpr int kBytes = kWarps * kWarpBytes;
+};
+
+// CTAs on an SM: what registers and rings allow.
+constexpr int resident(int hd) { return hd <= 64 ? 3 : 2; }
 
 template <int HD>  // head_dim <= HD
 __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs a, bool bf16) {
-  constexpr int kBatch = HD <= 128 ? 32 : 16, kBatches = 32 / kBatch;  // tokens under way at once
-  constexpr int kKeyWords = HD / 16, kValueWords = HD / 32;            // of a lane's part of a row
+  using R = Ring<HD>;
+  constexpr int kBatch = R::kBatch, kBatches = 32 / kBatch, kSumStride = HD + 8;
+  static_assert(8 * kSumStride * 4 <= R::kWarpBytes, "a warp's sums take the place of its ring");
+  extern __shared__ __align__(16) uint8_t ring[];
   __shared__ long long scratch[NT + 4];
   __shared__ float ml[kWarps][2][8];
-  __shared__ float sums[kWarps][8][HD];
   __shared__ uint4 queries[HD / 16][32];  // the same for every warp
   __shared__ int err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hi = lane >> 2, c = lane & 3;
   const int hd = a.hd, G = a.G;
-  const int key_dim = c * (HD / 4), key_bytes = max(0, min(HD / 4, hd - key_dim));
   const int value_dim = hi * (HD / 8), value_bytes = max(0, min(HD / 8, hd - value_dim));
   const bool wide = hd % 16 == 0;
+  const uint32_t my_ring = (uint32_t)__cvta_generic_to_shared(ring) + warp * R::kWarpBytes;
+  auto sums = [&](int w, int g) { return reinterpret_cast<float*>(ring + w * R::kWarpBytes) + g * kSumStride; };
   if (tid == 0) err = 0;
+  prefetch_inputs(a);
   grid_dependency();
   Walk k(a, find_work<NT>(a, scratch));
   while (k.next()) {
     const int* table = a.table + (size_t)k.b * a.max_pages;
     const size_t row0 = ((size_t)k.b * a.Hkv + k.h) * G;
 
+    // batch i of the range is batch i % kBatches of the warp's tokens of tile tile0 + i / kBatches
+    const int n_batches = (k.tile1 - k.tile0) * kBatches;
+    struct Part {  // a batch's page (-1: none) and the tokens that are attended, counted from its first: [from, to)
+      int id, from, to;
+      unsigned row;  // of its first token in the page
+      float ks, vs;
+    };
+    // a page id is on its way a batch before it is looked at, the scales and rows two before they are used
+    auto part_of = [&](int i) {
+      Part b{-1, 0, 0, 0, 0.f, 0.f};
+      if (i >= n_batches) return b;
+      const int t = (k.sp.page0 + (k.tile0 + i / kBatches) * kTilePages) * kBlock + warp * 32 + i % kBatches * kBatch;
+      if (t / kBlock * kBlock >= k.sp.n) return b;
+      b.id = __ldg(table + t / kBlock);
+      b.from = max(0, k.sp.lo - t);
+      b.to = min(kBatch, k.sp.n - t);
+      b.row = t % kBlock;
+      return b;
+    };
+    auto resolve = [&](Part& b) {
+      if ((unsigned)b.id < (unsigned)a.n_pages) {
+        b.ks = __ldg(a.ks + (size_t)b.id * a.Hkv + k.h);
+        b.vs = __ldg(a.vs + (size_t)b.id * a.Hkv + k.h);
+      } else {
+        if (lane == 0 && (b.to || b.from)) atomicOr(&err, LR_DEVERR_PAGE);
+        b.from = b.to = 0;
+      }
+    };
+    // A stage: of the keys, the rows of tokens 8 n + hi; of the values, those of tokens
+    // 16 n + {2c, 2c + 1, 2c + 8, 2c + 9}.
+    auto copy = [&](int i, const Part& b) {
+      if (b.to > b.from) {
+        const uint32_t to = my_ring + i % R::kStages * R::kStageBytes;
+        const size_t head = (size_t)b.id * a.page_stride + ((size_t)k.h * kBlock + b.row) * hd;
+        const uint8_t* keys = a.kc + head + (unsigned)(hi * hd + 16 * c);
+        const uint8_t* values = a.vc + head + (unsigned)(2 * c * hd + value_dim);
+#pragma unroll
+        for (int n = 0; n < kBatch / 8; ++n) {
+          const int t = 8 * n + hi, row_bytes = t >= b.from && t < b.to ? hd - 16 * c : 0;
+#pragma unroll
+          for (int x = 0; x < R::kKeyParts; ++x) {
+            const int bytes = max(0, min(16, row_bytes - 64 * x));
+            copy_part<16>(to + ((n * R::kKeyParts + x) * 32 + lane) * 16, bytes ? keys + (unsigned)(8 * n * hd) + 64 * x : a.kc,
+                          bytes, wide);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < kBatch / 4; ++n) {
+          const int row = n / 4 * 16 + (n & 1) + (n >> 1 & 1) * 8, t = 2 * c + row;
+          const int bytes = t >= b.from && t < b.to ? value_bytes : 0;
+#pragma unroll
+          for (int x = 0; x < R::kValueParts; ++x)
+            copy_part<R::kValueBytes>(to + R::kValues + ((n * R::kValueParts + x) * 32 + lane) * R::kValueBytes,
+                                      bytes > R::kValueBytes * x ? values + (unsigned)(row * hd) + R::kValueBytes * x : a.vc,
+                                      max(0, min(R::kValueBytes, bytes - R::kValueBytes * x)), wide);
+        }
+      }
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    Part now = part_of(0), next = part_of(1), after = part_of(2);
+    __syncthreads();  // the last segment's queries and sums have been read
+
     // head `hi` of the queries, the dims of this lane's keys: scaled to [2^14, 2^15) and split
-    __syncthreads();
     float factor;
     {
       float x[HD / 4], top = 0.f;
 #pragma unroll
       for (int d = 0; d < HD / 4; d += 4) {
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        const size_t at = (row0 + hi) * hd + key_dim + d;
-        if (hi < G && d < key_bytes) {
+        const int dim = d / 16 * 64 + 16 * c + d % 16;
+        const size_t at = (row0 + hi) * hd + dim;
+        if (hi < G && dim < hd) {
           if (bf16) {
             const uint2 u = __ldg(reinterpret_cast<const uint2*>((const __nv_bfloat16*)a.q + at));
             v = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
@@ -114,6 +192,10 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
         x[d + 3] = v.w;
         top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
       }
+      resolve(now);
+      copy(0, now);
+      resolve(next);
+      copy(1, next);
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 14, -112);
@@ -135,82 +217,36 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
     float m = -CUDART_INF_F, l = 0.f;  // of head `hi`; the sum is this lane's share
     float unit = 0.f, largest = 0.f;   // of the value scales so far
 
-    // batch i of the range is batch i % kBatches of the warp's tokens of tile tile0 + i / kBatches
-    const int n_batches = (k.tile1 - k.tile0) * kBatches;
-    struct Part {  // a batch's page (-1: none) and the tokens that are attended, counted from its first: [from, to)
-      int id, from, to;
-      unsigned row;  // of its first token in the page
-      float ks, vs;
-    };
-    // the page id is on its way a batch before it is looked at, the scales a batch before they are used
-    auto part_of = [&](int i) {
-      Part b{-1, 0, 0, 0, 0.f, 0.f};
-      if (i >= n_batches) return b;
-      const int t = (k.sp.page0 + (k.tile0 + i / kBatches) * kTilePages) * kBlock + warp * 32 + i % kBatches * kBatch;
-      if (t / kBlock * kBlock >= k.sp.n) return b;
-      b.id = __ldg(table + t / kBlock);
-      b.from = max(0, k.sp.lo - t);
-      b.to = min(kBatch, k.sp.n - t);
-      b.row = t % kBlock;
-      return b;
-    };
-    auto resolve = [&](Part& b) {
-      if ((unsigned)b.id < (unsigned)a.n_pages) {
-        b.ks = __ldg(a.ks + (size_t)b.id * a.Hkv + k.h);
-        b.vs = __ldg(a.vs + (size_t)b.id * a.Hkv + k.h);
-      } else {
-        if (lane == 0 && (b.to || b.from)) atomicOr(&err, LR_DEVERR_PAGE);
-        b.from = b.to = 0;
-      }
-    };
-    auto page_head = [&](const uint8_t* codes, const Part& b) {
-      return codes + (size_t)b.id * a.page_stride + ((size_t)k.h * kBlock + b.row) * hd;
-    };
-    // rows of the keys: token 8 n + hi
-    auto load_keys = [&](const Part& b, uint32_t (&w)[kBatch / 8][kKeyWords]) {
-      const bool any = b.to > b.from;
-      const uint8_t* at = any ? page_head(a.kc, b) + (unsigned)(hi * hd + key_dim) : nullptr;
-#pragma unroll
-      for (int n = 0; n < kBatch / 8; ++n) {
-        const int t = 8 * n + hi;
-        load_row<kKeyWords>(at + (unsigned)(8 * n * hd), any && t >= b.from && t < b.to ? key_bytes : 0, wide, w[n]);
-      }
-    };
-    // rows of the values: tokens 16 n + {2c, 2c + 1, 2c + 8, 2c + 9}
-    auto load_values = [&](const Part& b, uint32_t (&w)[kBatch / 16][4][kValueWords]) {
-      const bool any = b.to > b.from;
-      const uint8_t* at = any ? page_head(a.vc, b) + (unsigned)(2 * c * hd + value_dim) : nullptr;
-#pragma unroll
-      for (int n = 0; n < kBatch / 16; ++n)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int row = 16 * n + (x & 1) + (x >> 1) * 8, t = 2 * c + row;
-          load_row<kValueWords>(at + (unsigned)(row * hd), any && t >= b.from && t < b.to ? value_bytes : 0, wide, w[n][x]);
-        }
-    };
-    Part now = part_of(0), next = part_of(1);
-    uint32_t kw[kBatch / 8][kKeyWords], vw[kBatch / 16][4][kValueWords];
-    resolve(now);
-    load_keys(now, kw);
     for (int i = 0; i < n_batches; ++i) {
-      load_values(now, vw);
-      resolve(next);
+      resolve(after);
+      copy(i + 2, after);
+      const Part last = part_of(i + 3);
+      asm volatile("cp.async.wait_group 2;" ::: "memory");
+      const uint32_t stage = my_ring + i % R::kStages * R::kStageBytes;
+      const bool any = now.to > now.from;  // else the stage holds what it held
       float x[kBatch / 8][2];  // scores of tokens 8 n + 2c and 8 n + 2c + 1
       {
         float s[kBatch / 8][4] = {};
 #pragma unroll
-        for (int j = 0; j < HD / 16; ++j) {
-          const uint4 q = queries[j][lane];
+        for (int y = 0; y < R::kKeyParts; ++y) {
+          uint4 w[kBatch / 8];
 #pragma unroll
-          for (int n = 0; n < kBatch / 8; ++n) mma_f16(s[n], q.x, q.y, q.z, q.w, code_pair(kw[n][j]), code_pair(kw[n][j] >> 16));
+          for (int n = 0; n < kBatch / 8; ++n) w[n] = load16(stage + ((n * R::kKeyParts + y) * 32 + lane) * 16);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const uint4 q = queries[4 * y + j][lane];
+#pragma unroll
+            for (int n = 0; n < kBatch / 8; ++n) {
+              const uint32_t v = j == 0 ? w[n].x : j == 1 ? w[n].y : j == 2 ? w[n].z : w[n].w;
+              mma_f16(s[n], q.x, q.y, q.z, q.w, code_pair(v), code_pair(v >> 16));
+            }
+          }
         }
 #pragma unroll
         for (int n = 0; n < kBatch / 8; ++n)
 #pragma unroll
           for (int y = 0; y < 2; ++y) x[n][y] = fmaf(s[n][2 + y], 1.f / 2048.f, s[n][y]) * (factor * now.ks);
       }
-      load_keys(next, kw);
-      const Part after = part_of(i + 2);
       if (now.from > 0 || now.to < kBatch) {
 #pragma unroll
         for (int n = 0; n < kBatch / 8; ++n)
@@ -232,7 +268,7 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
       // sums are kept in units of the page's value scale, or of 2^-64 of the largest so far, so that
       // neither they nor the weights leave their type's range
       float share = 0.f;
-      if (now.to > now.from) {
+      if (any) {
         largest = fmaxf(largest, now.vs);
         const float u = fmaxf(now.vs, largest * 5.421010862427522e-20f);
         if (unit != u) old *= unit / u;
@@ -250,46 +286,61 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
         uint32_t p[4];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
-          const float p0 = exp2f(x[2 * n + y][0] - ref), p1 = exp2f(x[2 * n + y][1] - ref);
+          const float p0 = exp2_ftz(x[2 * n + y][0] - ref), p1 = exp2_ftz(x[2 * n + y][1] - ref);
           l += p0 + p1;
           split(p0 * share * 32768.f, p1 * share * 32768.f, p[2 * y], p[2 * y + 1]);
         }
+        if (!any) continue;
 #pragma unroll
-        for (int j = 0; j < HD / 8; j += 4) {
-          uint32_t b[2][4];  // of the rows 2c, 2c + 1 and of the rows 2c + 8, 2c + 9: pairs of dims j .. j + 3
+        for (int z = 0; z < R::kValueParts; ++z) {
+          uint32_t r[4][R::kValueBytes / 4];  // of the rows 2c, 2c + 1, 2c + 8 and 2c + 9
 #pragma unroll
-          for (int y = 0; y < 2; ++y) {
-            const uint32_t r0 = vw[n][2 * y][j / 4], r1 = vw[n][2 * y + 1][j / 4];
-            const uint32_t lo = __byte_perm(r0, r1, 0x5140), up = __byte_perm(r0, r1, 0x7362);
-            b[y][0] = code_pair(lo);
-            b[y][1] = code_pair(lo >> 16);
-            b[y][2] = code_pair(up);
-            b[y][3] = code_pair(up >> 16);
+          for (int y = 0; y < 4; ++y) {
+            const uint32_t at = stage + R::kValues + (((4 * n + y) * R::kValueParts + z) * 32 + lane) * R::kValueBytes;
+            if constexpr (R::kValueBytes == 16) {
+              const uint4 v = load16(at);
+              r[y][0] = v.x;
+              r[y][1] = v.y;
+              r[y][2] = v.z;
+              r[y][3] = v.w;
+            } else {
+              const uint2 v = load8(at);
+              r[y][0] = v.x;
+              r[y][1] = v.y;
+            }
           }
 #pragma unroll
-          for (int y = 0; y < 4; ++y) mma_f16(acc[j + y], p[0], p[1], p[2], p[3], b[0][y], b[1][y]);
+          for (int w = 0; w < R::kValueBytes / 4; ++w) {  // four dims: pairs of tokens
+            const uint32_t a0 = __byte_perm(r[0][w], r[1][w], 0x5140), a1 = __byte_perm(r[0][w], r[1][w], 0x7362);
+            const uint32_t b0 = __byte_perm(r[2][w], r[3][w], 0x5140), b1 = __byte_perm(r[2][w], r[3][w], 0x7362);
+            float(*to)[4] = acc + z * R::kValueBytes + 4 * w;
+            mma_f16(to[0], p[0], p[1], p[2], p[3], code_pair(a0), code_pair(b0));
+            mma_f16(to[1], p[0], p[1], p[2], p[3], code_pair(a0 >> 16), code_pair(b0 >> 16));
+            mma_f16(to[2], p[0], p[1], p[2], p[3], code_pair(a1), code_pair(b1));
+            mma_f16(to[3], p[0], p[1], p[2], p[3], code_pair(a1 >> 16), code_pair(b1 >> 16));
+          }
         }
       }
       now = next;
       next = after;
+      after = last;
     }
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
-    __syncthreads();  // the last segment's sums have been read
     if (c == 0) {
       ml[warp][0][hi] = m;
       ml[warp][1][hi] = l;
     }
+    // dim d of a head is at d % (HD / 8) * 8 + d / (HD / 8): no two lanes meet in a bank
     const float scale = unit * (1.f / 32768.f);
 #pragma unroll
-    for (int j = 0; j < HD / 8; ++j) {
-      sums[warp][hi][2 * c * (HD / 8) + j] = fmaf(acc[j][2], 1.f / 2048.f, acc[j][0]) * scale;
-      sums[warp][hi][(2 * c + 1) * (HD / 8) + j] = fmaf(acc[j][3], 1.f / 2048.f, acc[j][1]) * scale;
-    }
+    for (int j = 0; j < HD / 8; ++j)
+      *reinterpret_cast<float2*>(sums(warp, hi) + 8 * j + 2 * c) =
+          make_float2(fmaf(acc[j][2], 1.f / 2048.f, acc[j][0]) * scale, fmaf(acc[j][3], 1.f / 2048.f, acc[j][1]) * scale);
     __syncthreads();
     const bool whole = k.whole();
     float* slot = whole ? nullptr : a.part + (size_t)piece_slot(k.wk, k.seg_first) * a.part_stride;
-    for (int g = 0; g < G; ++g) {
+    for (int g = warp; g < G; g += kWarps) {
       float top = -CUDART_INF_F;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) top = fmaxf(top, ml[w][0][g]);
@@ -300,19 +351,21 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
         f[w] = exp2f(ml[w][0][g] - ref);
         sum = fmaf(ml[w][1][g], f[w], sum);
       }
-      Joined j;
+      Joined j{0.f, 0.f, 0.f};
       if (whole) {
         j = join_prev(a, row0 + g, top, sum);
-        __syncthreads();  // lse may be lse_prev: every thread has read it
-        if (a.lse && tid == 0) a.lse[row0 + g] = j.lse;
-      } else if (tid == 0) {
+        __syncwarp();  // lse may be lse_prev: every lane has read it
+        if (a.lse && lane == 0) a.lse[row0 + g] = j.lse;
+      } else if (lane == 0) {
         slot[G * hd + g] = top;
         slot[G * hd + 8 + g] = sum;
       }
-      for (int d = tid; d < hd; d += NT) {
+      for (int at = lane; at < HD; at += 32) {
+        const int d = at % 8 * (HD / 8) + at / 8;
+        if (d >= hd) continue;
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) v = fmaf(sums[w][g][d], f[w], v);
+        for (int w = 0; w < kWarps; ++w) v = fmaf(sums(w, g)[at], f[w], v);
         if (!whole) slot[g * hd + d] = v;
         else if (bf16) ((__nv_bfloat16*)a.o)[(row0 + g) * hd + d] = joined_value<__nv_bfloat16>(a, row0 + g, d, j, v);
         else ((float*)a.o)[(row0 + g) * hd + d] = joined_value<float>(a, row0 + g, d, j, v);
@@ -323,35 +376,41 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
   if (tid == 0) a.cta_err[blockIdx.x] = err;
 }
 
-void (*attn_kernel(int hd))(Kv8AttnArgs, bool) {
-  return hd <= 64 ? kv8_attn_kernel<64> : hd <= 128 ? kv8_attn_kernel<128> : kv8_attn_kernel<256>;
+template <int HD>
+cudaError_t launch_attn_hd(const Kv8AttnArgs& a, bool bf16, cudaStream_t st) {
+  const cudaError_t e = cudaFuncSetAttribute(kv8_attn_kernel<HD>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<HD>::kBytes);
+  if (e != cudaSuccess) return e;
+  return launch_overlapped(kv8_attn_kernel<HD>, dim3(a.n_cta), NT, Ring<HD>::kBytes, st, a, bf16);
+}
+cudaError_t launch_attn_any(const Kv8AttnArgs& a, bool bf16, cudaStream_t st) {
+  return a.hd <= 64 ? launch_attn_hd<64>(a, bf16, st) : a.hd <= 128 ? launch_attn_hd<128>(a, bf16, st) : launch_attn_hd<256>(a, bf16, st);
 }
 
 // ------------------------------------------------------------------ joining the pieces
 //
-// CTA (c, g): query head g of the segment that the range of CTA c of the attention kernel is the first to start inside
-// of (none, most of the time). Four numbers to a thread, the pieces spread over the rest of the threads,
+// CTA (c, y): every gridDim.y-th query head of the segment that the range of CTA c of the attention kernel is the
+// first to start inside of (none, most of the time). Four numbers to a thread, the pieces spread over the rest of the threads,
 // so that all of them are under way at once; the order of the sums is fixed by the threads. The same
 // grid answers the empty sequences, a row to a warp, and collects the device errors. It may be launched
 // while the attention kernel still runs: only lens is read before it has ended.
 
 constexpr int JT = 128;
-constexpr int kMaxCtas = 1024;
+constexpr int kMaxCtas = 1184;  // eight to an SM: as many as are there at once
 
 template <typename T>
-__global__ void __launch_bounds__(JT) kv8_join_kernel(Kv8AttnArgs a) {
+__global__ void __launch_bounds__(JT, 7) kv8_join_kernel(Kv8AttnArgs a) {
   __shared__ long long scratch[JT + 4];
   __shared__ float weight[kMaxCtas], sum_of[kMaxCtas];
   __shared__ float red[2][JT / 32];
   __shared__ __align__(16) float sums[JT * 4];
   __shared__ int err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int c = blockIdx.x, g = blockIdx.y, Hq = a.Hkv * a.G, hd = a.hd;
+  const int c = blockIdx.x, Hq = a.Hkv * a.G, hd = a.hd;
   const Work wk = find_work<JT>(a, scratch);
   Walk k(a, wk);
   // the first of the CTAs whose range starts inside the segment
   const bool mine = c > 0 && k.next() && k.tile0 > 0 && range_begin(wk.total, c - 1, wk.active) <= k.seg_first;
-  const bool errors = c == 0 && g == 0;
+  const bool errors = c == 0 && blockIdx.y == 0;
   if (errors) {
     if (tid == 0) err = 0;
     __syncthreads();
@@ -363,7 +422,7 @@ __global__ void __launch_bounds__(JT) kv8_join_kernel(Kv8AttnArgs a) {
     if (bad) atomicOr(&err, LR_DEVERR_LEN);
   }
   const long long n_warps = (long long)gridDim.x * gridDim.y * (JT / 32), rows = (long long)a.B * Hq;
-  for (long long row = ((long long)g * gridDim.x + c) * (JT / 32) + warp; row < rows; row += n_warps) {
+  for (long long row = ((long long)blockIdx.y * gridDim.x + c) * (JT / 32) + warp; row < rows; row += n_warps) {
     if (__ldg(a.lens + row / Hq) > 0) continue;
     const Joined j = join_prev(a, row, -CUDART_INF_F, 0.f);
     for (int d = lane; d < hd; d += 32) ((T*)a.o)[row * hd + d] = joined_value<T>(a, row, d, j, 0.f);
@@ -380,67 +439,72 @@ __global__ void __launch_bounds__(JT) kv8_join_kernel(Kv8AttnArgs a) {
   }
   if (!mine) return;
   const Pieces pc = pieces_of(k);
-  const size_t row = ((size_t)k.b * a.Hkv + k.h) * a.G + g;
-  const int n = pc.n, ml = a.G * hd + g;
+  const int n = pc.n;
   const int cols = hd / 4, groups = JT / cols, col = tid % cols, group = tid / cols;
-  auto values = [&](int i) {
-    return __ldcg(reinterpret_cast<const float4*>(a.part + (size_t)pc.slot(i) * a.part_stride + g * hd) + col);
-  };
-  // a thread's first pieces are on their way before their weights are known
-  constexpr int kAhead = 10;
-  float4 v[kAhead];
-#pragma unroll
-  for (int x = 0; x < kAhead; ++x) {
-    const int i = group + x * groups;
-    v[x] = group < groups && i < n ? values(i) : make_float4(0.f, 0.f, 0.f, 0.f);
-  }
-  float m = -CUDART_INF_F;
-  for (int i = tid; i < n; i += JT) {
-    const float* at = a.part + (size_t)pc.slot(i) * a.part_stride + ml;
-    const float mi = __ldcg(at);
-    sum_of[i] = __ldcg(at + 8);
-    weight[i] = mi;
-    m = fmaxf(m, mi);
-  }
-  m = warp_max(m);
-  if (lane == 0) red[0][warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  const float ref = m == -CUDART_INF_F ? 0.f : m;
-  float l = 0.f;
-  for (int i = tid; i < n; i += JT) {
-    const float w = exp2f(weight[i] - ref);
-    weight[i] = w;
-    l = fmaf(w, sum_of[i], l);
-  }
-  l = warp_sum(l);
-  if (lane == 0) red[1][warp] = l;
-  __syncthreads();
-  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  if (group < groups) {
-    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-    auto add = [&](int i, const float4& x) {
-      const float w = weight[i];
-      s.x = fmaf(w, x.x, s.x);
-      s.y = fmaf(w, x.y, s.y);
-      s.z = fmaf(w, x.z, s.z);
-      s.w = fmaf(w, x.w, s.w);
+#pragma unroll 1
+  for (int g = blockIdx.y; g < a.G; g += gridDim.y) {
+    const size_t row = ((size_t)k.b * a.Hkv + k.h) * a.G + g;
+    const int ml = a.G * hd + g;
+    auto values = [&](int i) {
+      return __ldcg(reinterpret_cast<const float4*>(a.part + (size_t)pc.slot(i) * a.part_stride + g * hd) + col);
     };
+    // a thread's first pieces are on their way before their weights are known
+    constexpr int kAhead = 10;
+    float4 v[kAhead];
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x)
-      if (group + x * groups < n) add(group + x * groups, v[x]);
+    for (int x = 0; x < kAhead; ++x) {
+      const int i = group + x * groups;
+      v[x] = group < groups && i < n ? values(i) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    float m = -CUDART_INF_F;
+    for (int i = tid; i < n; i += JT) {
+      const float* at = a.part + (size_t)pc.slot(i) * a.part_stride + ml;
+      const float mi = __ldcg(at);
+      sum_of[i] = __ldcg(at + 8);
+      weight[i] = mi;
+      m = fmaxf(m, mi);
+    }
+    m = warp_max(m);
+    if (lane == 0) red[0][warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float ref = m == -CUDART_INF_F ? 0.f : m;
+    float l = 0.f;
+    for (int i = tid; i < n; i += JT) {
+      const float w = exp2f(weight[i] - ref);
+      weight[i] = w;
+      l = fmaf(w, sum_of[i], l);
+    }
+    l = warp_sum(l);
+    if (lane == 0) red[1][warp] = l;
+    __syncthreads();
+    l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    if (group < groups) {
+      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+      auto add = [&](int i, const float4& x) {
+        const float w = weight[i];
+        s.x = fmaf(w, x.x, s.x);
+        s.y = fmaf(w, x.y, s.y);
+        s.z = fmaf(w, x.z, s.z);
+        s.w = fmaf(w, x.w, s.w);
+      };
+#pragma unroll
+      for (int x = 0; x < kAhead; ++x)
+        if (group + x * groups < n) add(group + x * groups, v[x]);
 #pragma unroll 4
-    for (int i = group + kAhead * groups; i < n; i += groups) add(i, values(i));
-    reinterpret_cast<float4*>(sums)[group * cols + col] = s;
+      for (int i = group + kAhead * groups; i < n; i += groups) add(i, values(i));
+      reinterpret_cast<float4*>(sums)[group * cols + col] = s;
+    }
+    const Joined j = join_prev(a, row, m, l);
+    __syncthreads();  // lse may be lse_prev: every thread has read it
+    for (int d = tid; d < hd; d += JT) {
+      float acc = 0.f;
+      for (int x = 0; x < groups; ++x) acc += sums[x * hd + d];
+      ((T*)a.o)[row * hd + d] = joined_value<T>(a, row, d, j, acc);
+    }
+    if (a.lse && tid == 0) a.lse[row] = j.lse;
+    __syncthreads();  // the next head uses the same shared memory
   }
-  const Joined j = join_prev(a, row, m, l);
-  __syncthreads();  // lse may be lse_prev: every thread has read it
-  for (int d = tid; d < hd; d += JT) {
-    float acc = 0.f;
-    for (int x = 0; x < groups; ++x) acc += sums[x * hd + d];
-    ((T*)a.o)[row * hd + d] = joined_value<T>(a, row, d, j, acc);
-  }
-  if (a.lse && tid == 0) a.lse[row] = j.lse;
 }
 
 template <typename T>
@@ -451,10 +515,10 @@ cudaError_t launch_attn(const Kv8AttnArgs& a, const Kv8AttnPlan& plan, cudaStrea
     if (!kv8_page_map(&mk, a.kc, a) || !kv8_page_map(&mv, a.vc, a)) return cudaErrorInvalidValue;
     e = launch_attn_tc(a, mk, mv, st);
   } else {
-    e = launch_overlapped(attn_kernel(a.hd), dim3(plan.n_cta), NT, 0, st, a, sizeof(T) == 2);
+    e = launch_attn_any(a, sizeof(T) == 2, st);
   }
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kv8_join_kernel<T>, dim3(plan.n_cta, a.G), JT, 0, st, a);
+  return launch_overlapped(kv8_join_kernel<T>, dim3(plan.n_cta, std::max(1, std::min(a.G, kMaxCtas / plan.n_cta))), JT, 0, st, a);
 }
 
 }  // namespace

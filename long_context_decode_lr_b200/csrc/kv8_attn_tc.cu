@@ -168,12 +168,14 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
   while (ok && unit - (lane >> 1) < wk.end) {
     const Batch t = next;
     const int id1 = __shfl_xor_sync(0xffffffffu, t.id, 1);
-    const float ks1 = __shfl_xor_sync(0xffffffffu, t.ks, 1), vs1 = __shfl_xor_sync(0xffffffffu, t.vs, 1);
+    float ks1, vs1;
     uint32_t live = __ballot_sync(0xffffffffu, t.live) & 0x55555555u;
-    batch_ids(a, wk, unit + 16, next);
     for (int x = 0; x < 16; ++x) {
       if (x == 8) batch_scales(a, sh, next);
-      if (!live) continue;
+      if (!live) {
+        if (x == 0) batch_ids(a, wk, unit + 16, next);
+        continue;
+      }
       const int src = __ffs(live) - 1;
       live &= live - 1;
       const uint32_t s = it % kStages, ph = (it / kStages) & 1;
@@ -181,9 +183,9 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
       ++it;
       const bool first = t.at.tile == 0 || unit == wk.begin;
       seg += __shfl_sync(0xffffffffu, first, src);
+      const bool last = t.at.tile == t.at.sp.tiles - 1 || unit == wk.end - 1;
+      const int head = t.at.b * a.Hkv + t.at.h, row = t.at.h * kBlock;
       if (lane == src) {
-        const bool last = t.at.tile == t.at.sp.tiles - 1 || unit == wk.end - 1;
-        const int head = t.at.b * a.Hkv + t.at.h, row = t.at.h * kBlock;
         const uint32_t bytes = ((t.id >= 0) + (id1 >= 0)) * kPageBytes, q_bytes = a.G * kHd * 2;
         uint64_t *kf = sh.bar(K_FULL + s), *vf = sh.bar(V_FULL + s);
         mbar_arrive_expect_tx(kf, bytes + (first ? q_bytes : 0));
@@ -194,6 +196,13 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
         mbar_arrive_expect_tx(vf, bytes);
         if (t.id >= 0) tma_load_3d(sh.values(s), mv, vf, 0, row, t.id);
         if (id1 >= 0) tma_load_3d(sh.values(s) + kPageBytes, mv, vf, 0, row, id1);
+      }
+      if (x == 0) {  // with the first tile on its way
+        batch_ids(a, wk, unit + 16, next);
+        ks1 = __shfl_xor_sync(0xffffffffu, t.ks, 1);
+        vs1 = __shfl_xor_sync(0xffffffffu, t.vs, 1);
+      }
+      if (lane == src) {
         Meta m;
         m.ks[0] = t.ks;
         m.ks[1] = ks1;
@@ -207,7 +216,7 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
         m.head = head;
         m.slot = piece_slot(wk, t.at.seg_first);
         *sh.meta(s) = m;
-        mbar_arrive(kf);
+        mbar_arrive(sh.bar(K_FULL + s));
       }
       __syncwarp();
     }
@@ -555,6 +564,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     tmem_relinquish();
   }
   tc_fence_before();
+  prefetch_inputs(a);
   grid_dependency();
   const Work wk = find_work<threads_of(GROUPS)>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
   tc_fence_after();

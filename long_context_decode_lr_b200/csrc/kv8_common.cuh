@@ -120,6 +120,16 @@ __device__ __forceinline__ long long range_begin(long long total, int c, int act
   return total * c / active;
 }
 
+// The lengths and the page table on their way to L2 while the grid before may still run: they are read one after the
+// other at the start, and after a step over many bytes they are in HBM again. Nothing is read
+// here, so it does not matter who is still writing them.
+__device__ __forceinline__ void prefetch_inputs(const Kv8AttnArgs& a) {
+  const long long line = (long long)blockIdx.x * blockDim.x + threadIdx.x;
+  const long long ids = (long long)a.B * a.max_pages;
+  if (line * 32 < ids) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + line * 32));
+  if (line * 32 < a.B) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.lens + line * 32));
+}
+
 // A CTA's range of units and where it starts.
 struct Work {
   long long begin, end;
