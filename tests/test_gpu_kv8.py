@@ -103,6 +103,10 @@ APPENDS = {
     "hd256": dict(new=[65], before=[10], hkv=1, hq=2, hd=256, rot=256, inter=False),
     "hd40": dict(new=[65, 2], before=[10, 0], hkv=2, hq=2, hd=40, rot=16, inter=False),
     "hd8": dict(new=[7], before=[0], hkv=1, hq=1, hd=8, rot=0, inter=False, dtype="f32"),
+    "hd96_half_rotated": dict(new=[70, 5], before=[10, 0], hkv=3, hq=9, hd=96, rot=48, inter=False),
+    "hd72_interleaved": dict(new=[65], before=[3], hkv=1, hq=3, hd=72, rot=64, inter=True),
+    "fp32_hd256": dict(new=[100], before=[7], hkv=2, hq=2, hd=256, rot=256, inter=False, dtype="f32"),
+    "more_heads_than_shares": dict(new=[130, 1, 64], before=[0, 63, 64], hkv=11, hq=22, hd=64, rot=64, inter=True),
     "many_short": dict(new=[2] * 40, before=list(range(40)), hkv=1, hq=1, hd=64, rot=64, inter=False),
     "one_each": dict(new=None, before=[0, 63, 64, 17, 200], hkv=2, hq=8, hd=128, rot=128, inter=False),
     "one_each_interleaved_f32": dict(new=None, before=[1, 0, 130], hkv=2, hq=4, hd=64, rot=32, inter=True, dtype="f32"),
@@ -264,6 +268,39 @@ def test_append_bad_data_is_reported_and_skipped():
         assert run_append(pool, k, k, k, cu, 128, False)[1] & lr.LR_DEVERR_LEN
 
 
+def test_append_refuses_overlapping_tokens():
+    """One row for every token (a broadcast view) is not a cache's input."""
+    pool = Pool(np.random.default_rng(8), [3], 2, 128)
+    k = torch.zeros((1, 2, 128), dtype=torch.bfloat16, device="cuda").expand(3, -1, -1)
+    v = torch.zeros((3, 2, 128), dtype=torch.bfloat16, device="cuda")
+    cu = torch.tensor([0, 3], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        lr.lr_kv8_append(pool.kv, k, v, lr.workspace(256), cu_tokens=cu)
+
+
+def test_append_two_calls_at_once():
+    """Two streams append to pages of their own in one pool at the same time."""
+    rng = np.random.default_rng(9)
+    new = [150, 90]
+    pool = Pool(rng, [0, 0], 2, 128, room=new)
+    before = pool.arrays()
+    k, kr = rounded(rng.standard_normal((sum(new), 2, 128)), "bf16")
+    v, vr = rounded(rng.standard_normal((sum(new), 2, 128)), "bf16")
+    pool.set_lens(new)
+    rope = lr.Rope(torch.from_numpy(inv_freq(128)).cuda(), 128)
+    kvs = [lr.Kv8Pages(*pool.dev[:4], pool.dev[4][b:b + 1].clone(), torch.tensor([new[b]], dtype=torch.int32, device="cuda"),
+                       torch.bfloat16) for b in range(2)]
+    parts = [slice(0, new[0]), slice(new[0], None)]
+    cus = [torch.tensor([0, n], dtype=torch.int32, device="cuda") for n in new]
+    streams, ws = [torch.cuda.Stream() for _ in range(2)], [lr.workspace(256) for _ in range(2)]
+    torch.cuda.synchronize()
+    for b in range(2):
+        lr.lr_kv8_append(kvs[b], k[parts[b]], v[parts[b]], ws[b], cu_tokens=cus[b], rope=rope, stream=streams[b])
+    torch.cuda.synchronize()
+    assert all(lr.lr_get_device_error(w) == 0 for w in ws)
+    check_append(pool, before, kr, vr, None, None, [0, new[0], sum(new)], 128, False)
+
+
 def test_append_empty_slots_and_nothing():
     rng = np.random.default_rng(7)
     pool = Pool(rng, [0, 5, 0], 1, 128, room=[64, 64, 64])
@@ -304,6 +341,15 @@ ATTN = {
     "f32_hd40_joined": dict(lens=[150, 0], hkv=2, G=3, hd=40, dtype="f32", prev=True, window=70),
     "bf16_hd64": dict(lens=[500, 3], hkv=2, G=4, hd=64),
     "bf16_hd8": dict(lens=[100], hkv=1, G=2, hd=8),
+    "f32_hd96_gqa8": dict(lens=[700, 64, 0, 33], hkv=2, G=8, hd=96, dtype="f32"),
+    "f32_hd120_window": dict(lens=[500, 31], hkv=1, G=5, hd=120, dtype="f32", window=77),
+    "f32_hd128_split": dict(lens=[6000], hkv=1, G=4, hd=128, dtype="f32"),
+    "f32_hd200_joined": dict(lens=[130, 0, 1], hkv=2, G=7, hd=200, dtype="f32", prev=True),
+    "bf16_hd96_joined": dict(lens=[260, 17], hkv=1, G=8, hd=96, prev=True, window=100),
+    "bf16_hd72": dict(lens=[129, 64, 63], hkv=2, G=1, hd=72),
+    "more_sequences_than_threads": dict(lens=[(7 * i) % 5 for i in range(700)], hkv=1, G=2),
+    "more_sequences_than_threads_f32": dict(lens=[(7 * i) % 5 for i in range(300)], hkv=1, G=2, hd=64, dtype="f32"),
+    "short_segments_gqa8": dict(lens=[1 + i % 130 for i in range(90)], hkv=8, G=8),
     "bf16_hd256": dict(lens=[100, 64], hkv=2, G=4, hd=256),
 }
 
@@ -350,6 +396,74 @@ def test_attention_scales_far_apart():
     o, lse, _ = attend(pool, q)
     ref = orc.decode(qr, pool.kc, pool.vc, pool.ks, pool.vs, pool.table, pool.lens, 128 ** -0.5)
     check_attention((o, lse), ref, pool, qr, 128 ** -0.5, 400)
+
+
+@pytest.mark.parametrize("hd,dtype", [(128, "bf16"), (64, "f32"), (256, "bf16")])
+def test_attention_scales_of_any_size(hd, dtype):
+    """Scales that are no powers of two and far apart, 1e-7 to 1e30, in any order, keys and values."""
+    rng = np.random.default_rng(16)
+    pool = Pool(rng, [64 * 9, 64 * 3 + 5], 2, hd, dtype)
+    for b in range(2):
+        for i in range(-(-int(pool.lens[b]) // 64)):
+            page = pool.table[b, i]
+            pool.vs[page] = rng.choice([1e-7, 3e-3, 0.7, 19.0, 1e8, 1e30], 2)
+            pool.ks[page] = rng.uniform(0.001, 0.02, 2)
+    pool.upload()
+    q, qr = rounded(rng.standard_normal((2, 8, hd)), dtype)
+    o, lse, err = attend(pool, q)
+    assert err == 0
+    scale = hd ** -0.5
+    ref = orc.decode(qr, pool.kc, pool.vc, pool.ks, pool.vs, pool.table, pool.lens, scale)
+    check_attention((o, lse), ref, pool, qr, scale, 600)
+
+
+def test_attention_result_does_not_depend_on_the_rest_of_the_batch():
+    """Room in the page table, unused pages and a workspace full of other bytes change nothing."""
+    rng = np.random.default_rng(17)
+    pool = Pool(rng, [500, 40], 2, 128)
+    q, _ = rounded(rng.standard_normal((2, 8, 128)), "bf16")
+    o, lse, _ = attend(pool, q)
+    wide = torch.full((2, 4000), 2 ** 31 - 1, dtype=torch.int32, device="cuda")
+    wide[:, :pool.width] = pool.dev[4]
+    kv = lr.Kv8Pages(*pool.dev[:4], wide, pool.dev[5], torch.bfloat16)
+    for fill in (0, 255):
+        ws = torch.full((lr.lr_kv8_attn_workspace_bytes(kv, 8),), fill, dtype=torch.uint8, device="cuda")
+        o2, lse2 = torch.full_like(o, 3.0), torch.full_like(lse, 3.0)
+        lr.lr_decode_attn_kv8(kv, 8, q, o2, ws, lse=lse2)
+        assert lr.lr_get_device_error(ws) == 0
+        # another width divides the work into other pieces: equal to the sums' rounding
+        torch.testing.assert_close(o2.float(), o.float(), rtol=2.0 ** -7, atol=2.0 ** -9)
+        torch.testing.assert_close(lse2, lse, rtol=1e-6, atol=1e-5)
+
+
+@pytest.mark.parametrize("hd,dtype", [(128, "bf16"), (64, "f32")])
+def test_attention_over_nothing(hd, dtype):
+    """No sequence has a token: 0 and -inf, or the earlier part as it is."""
+    pool = Pool(np.random.default_rng(19), [0, 0, 0], 2, hd, dtype)
+    q = torch.ones((3, 8, hd), dtype=DT[dtype], device="cuda")
+    o, lse, err = attend(pool, q)
+    assert err == 0 and (o == 0).all() and torch.isneginf(lse).all()
+    prev = (torch.randn_like(q), torch.randn((3, 8), device="cuda"))
+    prev[1][1] = float("-inf")
+    o, lse, err = attend(pool, q, prev=prev)
+    assert err == 0 and (o[1] == 0).all() and torch.equal(o[[0, 2]], prev[0][[0, 2]])
+    torch.testing.assert_close(lse, prev[1], rtol=2.0 ** -22, atol=2.0 ** -22)
+
+
+def test_attention_infinite_query():
+    """A head with an infinite query number gives NaN, the other heads of the KV head are as without it."""
+    rng = np.random.default_rng(18)
+    for hd, dtype in ((128, "bf16"), (64, "f32")):
+        pool = Pool(rng, [200, 30], 1, hd, dtype)
+        q, _ = rounded(rng.standard_normal((2, 4, hd)), dtype)
+        o, lse, _ = attend(pool, q)
+        bad = q.clone()
+        bad[0, 2, 5] = float("inf")
+        o2, lse2, err = attend(pool, bad)
+        assert err == 0 and torch.isnan(o2[0, 2]).all() and torch.isnan(lse2[0, 2])
+        keep = torch.ones(2, 4, dtype=torch.bool, device="cuda")
+        keep[0, 2] = False
+        assert torch.equal(o2[keep], o[keep]) and torch.equal(lse2[keep], lse[keep])
 
 
 def test_attention_extreme_scores():
