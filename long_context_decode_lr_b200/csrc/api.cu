@@ -584,6 +584,7 @@ lr_status lr_decode_attn_kv8(const lr_kv8_pages* kv, int32_t n_q_heads, const vo
   a.q = q; a.o_prev = o_prev; a.lse_prev = lse_prev; a.o = o; a.lse = lse;
   a.err = (int*)ws;
   a.cta_err = (int*)((char*)ws + plan.cta_err_off);
+  a.split = (char*)ws + plan.split_off;
   a.part = (float*)((char*)ws + plan.part_off);
   a.n_cta = plan.n_cta;
   a.part_stride = plan.part_stride;

@@ -102,6 +102,8 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
   prefetch_inputs(a);
   grid_dependency();
   Walk k(a, find_work<NT>(a, scratch));
+  if (blockIdx.x == 0 && k.wk.bad_len) atomicOr(&err, LR_DEVERR_LEN);
+  if (tid == 0) write_pieces(a, k.wk);
   while (k.next()) {
     const int* table = a.table + (size_t)k.b * a.max_pages;
     const size_t row0 = ((size_t)k.b * a.Hkv + k.h) * G;
@@ -372,6 +374,8 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
       }
     }
   }
+  if (bf16) empty_rows<__nv_bfloat16>(a, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
+  else empty_rows<float>(a, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
   __syncthreads();
   if (tid == 0) a.cta_err[blockIdx.x] = err;
 }
@@ -388,62 +392,40 @@ cudaError_t launch_attn_any(const Kv8AttnArgs& a, bool bf16, cudaStream_t st) {
 
 // ------------------------------------------------------------------ joining the pieces
 //
-// CTA (c, y): every gridDim.y-th query head of the segment that the range of CTA c of the attention kernel is the
-// first to start inside of (none, most of the time). Four numbers to a thread, the pieces spread over the rest of the threads,
-// so that all of them are under way at once; the order of the sums is fixed by the threads. The same
-// grid answers the empty sequences, a row to a warp, and collects the device errors. It may be launched
-// while the attention kernel still runs: only lens is read before it has ended.
+// CTA (c, y): every gridDim.y-th query head of the segment that CTA c of the attention kernel wrote down (none,
+// most of the time). Four numbers to a thread, the pieces spread over the rest of the threads, so that all of
+// them are under way at once; the order of the sums is fixed by the threads. CTA (0, 0) collects the
+// device errors too.
 
 constexpr int JT = 128;
 constexpr int kMaxCtas = 1184;  // eight to an SM: as many as are there at once
 
 template <typename T>
 __global__ void __launch_bounds__(JT, 7) kv8_join_kernel(Kv8AttnArgs a) {
-  __shared__ long long scratch[JT + 4];
   __shared__ float weight[kMaxCtas], sum_of[kMaxCtas];
   __shared__ float red[2][JT / 32];
   __shared__ __align__(16) float sums[JT * 4];
   __shared__ int err;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int c = blockIdx.x, Hq = a.Hkv * a.G, hd = a.hd;
-  const Work wk = find_work<JT>(a, scratch);
-  Walk k(a, wk);
-  // the first of the CTAs whose range starts inside the segment
-  const bool mine = c > 0 && k.next() && k.tile0 > 0 && range_begin(wk.total, c - 1, wk.active) <= k.seg_first;
-  const bool errors = c == 0 && blockIdx.y == 0;
-  if (errors) {
-    if (tid == 0) err = 0;
-    __syncthreads();
-    bool bad = false;
-    for (int b = tid; b < a.B; b += JT) {
-      const int len = __ldg(a.lens + b);
-      bad |= len < 0 || len > a.max_pages * kBlock;
-    }
-    if (bad) atomicOr(&err, LR_DEVERR_LEN);
-  }
-  const long long n_warps = (long long)gridDim.x * gridDim.y * (JT / 32), rows = (long long)a.B * Hq;
-  for (long long row = ((long long)blockIdx.y * gridDim.x + c) * (JT / 32) + warp; row < rows; row += n_warps) {
-    if (__ldg(a.lens + row / Hq) > 0) continue;
-    const Joined j = join_prev(a, row, -CUDART_INF_F, 0.f);
-    for (int d = lane; d < hd; d += 32) ((T*)a.o)[row * hd + d] = joined_value<T>(a, row, d, j, 0.f);
-    __syncwarp();
-    if (a.lse && lane == 0) a.lse[row] = j.lse;
-  }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hd = a.hd;
+  const bool errors = blockIdx.x == 0 && blockIdx.y == 0;
+  if (errors && tid == 0) err = 0;
   grid_dependency();
   if (errors) {
     int bits = 0;
     for (int i = tid; i < a.n_cta; i += JT) bits |= __ldcg(a.cta_err + i);
+    __syncthreads();
     if (bits) atomicOr(&err, bits);
     __syncthreads();
     if (tid == 0) *a.err = err;
   }
-  if (!mine) return;
-  const Pieces pc = pieces_of(k);
+  const int4 said = __ldcg(reinterpret_cast<const int4*>(a.split) + blockIdx.x);
+  const Pieces pc{said.x, said.y, said.z, said.w};
   const int n = pc.n;
+  if (n == 0) return;
   const int cols = hd / 4, groups = JT / cols, col = tid % cols, group = tid / cols;
 #pragma unroll 1
   for (int g = blockIdx.y; g < a.G; g += gridDim.y) {
-    const size_t row = ((size_t)k.b * a.Hkv + k.h) * a.G + g;
+    const size_t row = (size_t)pc.head * a.G + g;
     const int ml = a.G * hd + g;
     auto values = [&](int i) {
       return __ldcg(reinterpret_cast<const float4*>(a.part + (size_t)pc.slot(i) * a.part_stride + g * hd) + col);
@@ -531,8 +513,9 @@ Kv8AttnPlan plan_kv8_attn(const lr_kv8_pages& kv, int n_q_heads, int sm_count) {
   p.tensor = kv.dtype == LR_BF16 && kv.head_dim == 128;
   p.n_cta = (int)std::max(1LL, std::min<long long>(most, std::min((p.tensor ? 2 : kv8::resident(kv.head_dim)) * sm_count, kv8::kMaxCtas)));
   p.part_stride = G * kv.head_dim + 16;
-  p.cta_err_off = 256;
-  p.part_off = (256 + (size_t)p.n_cta * sizeof(int) + 255) & ~(size_t)255;
+  p.split_off = 256;
+  p.cta_err_off = p.split_off + (size_t)p.n_cta * sizeof(kv8::Pieces);
+  p.part_off = (p.cta_err_off + (size_t)p.n_cta * sizeof(int) + 255) & ~(size_t)255;
   p.ws_bytes = p.part_off + (((size_t)2 * p.n_cta * p.part_stride * sizeof(float) + 255) & ~(size_t)255);
   return p;
 }

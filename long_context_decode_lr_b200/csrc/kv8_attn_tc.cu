@@ -531,7 +531,10 @@ __global__ void __launch_bounds__(threads_of(GROUPS), 2)
 kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv, const Kv8AttnArgs a) {
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
-    if (threadIdx.x == 0) a.cta_err[blockIdx.x] = LR_DEVERR_LAUNCH;
+    if (threadIdx.x == 0) {
+      a.cta_err[blockIdx.x] = LR_DEVERR_LAUNCH;
+      reinterpret_cast<Pieces*>(a.split)[blockIdx.x] = Pieces{0, 0, 0, 0};
+    }
     return;
   }
   const Shared sh{smem};
@@ -567,12 +570,16 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   prefetch_inputs(a);
   grid_dependency();
   const Work wk = find_work<threads_of(GROUPS)>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
+  if (blockIdx.x == 0 && wk.bad_len) atomicOr(sh.err(), LR_DEVERR_LEN);
   tc_fence_after();
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   if (warp < kLoads) {
     attend<GROUPS>(a, sh, tmem);
   } else if (warp == kLoads) {
     load_tiles(a, sh, &mk, &mv, wk);
+    if (lane == 0) write_pieces(a, wk);
+    __syncwarp();
+    empty_rows<__nv_bfloat16>(a, blockIdx.x, gridDim.x);
   } else {
     issue_products<GROUPS>(a, sh, tmem);
   }

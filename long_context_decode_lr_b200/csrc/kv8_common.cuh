@@ -89,9 +89,10 @@ __device__ __forceinline__ float exp2_ftz(float x) {
 // takes units [c W / C, (c + 1) W / C), so ragged lengths cost nothing and one long sequence
 // fills the machine. A CTA's range touches at most two segments that others share: its first
 // and its last one. What it has of those are pieces (unnormalised sums with their maximum) in the
-// slots 2c and 2c + 1; a second kernel joins a segment's pieces in the order of the CTAs. (Joined by the
-// last CTA to finish instead, one of them was busy for 5 us with 8 pieces and 20 us with 37, its own
-// tiles waiting.)
+// slots 2c and 2c + 1; a second kernel joins a segment's pieces in the order of the CTAs, which it finds
+// written down: CTA c does so for the segment that its range is the first to start inside of. (Joined by
+// the last CTA to finish instead, one of them was busy for 5 us with 8 pieces and 20 us with 37, its
+// own tiles waiting; with the division worked out again in the second kernel, that one took 6 us.)
 
 constexpr int kTilePages = 2;
 constexpr int kTileTokens = kTilePages * kBlock;
@@ -137,6 +138,7 @@ struct Work {
   int active;            // CTAs that have a range
   int b;                 // sequence of the first unit
   long long b_first;     // first unit of that sequence
+  bool bad_len;          // this thread has seen a length out of bounds
 };
 
 // Called by all NT threads of the CTA; `scratch` holds NT + 4 long longs of shared memory.
@@ -145,7 +147,13 @@ __device__ __forceinline__ Work find_work(const Kv8AttnArgs& a, long long* scrat
   const int tid = threadIdx.x;
   const int per = (a.B + NT - 1) / NT, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   long long mine = 0;
-  for (int b = b0; b < b1; ++b) mine += (long long)seq_span(a, b).units * a.Hkv;
+  Work wk;
+  wk.bad_len = false;
+  for (int b = b0; b < b1; ++b) {
+    mine += (long long)seq_span(a, b).units * a.Hkv;
+    const int len = __ldg(a.lens + b);
+    wk.bad_len |= len < 0 || len > a.max_pages * kBlock;
+  }
   // inclusive scan over the warp, then over the warps
   long long run = mine;
   const int lane = tid & 31, warp = tid >> 5;
@@ -163,7 +171,6 @@ __device__ __forceinline__ Work find_work(const Kv8AttnArgs& a, long long* scrat
     total += scratch[w];
   }
   const long long first = before + run - mine;
-  Work wk;
   wk.total = total;
   wk.active = (int)min((long long)a.n_cta, total);
   const int c = blockIdx.x;
@@ -286,20 +293,47 @@ __device__ __forceinline__ int piece_slot(const Work& wk, long long seg_first) {
   return 2 * blockIdx.x + (wk.begin < seg_first ? 1 : 0);
 }
 
-// The CTAs that share a segment, and the slot of each one's piece.
-struct Pieces {
-  int c0, n;
-  bool mid;  // the first CTA's range starts before the segment: its piece is its second one
+// A split segment: b * Hkv + h, the CTAs that share it, and whether the first one's range starts before it (its
+// piece is its second one then).
+struct __align__(16) Pieces {
+  int head, n, c0, mid;
   __device__ int slot(int i) const { return 2 * (c0 + i) + (i == 0 && mid ? 1 : 0); }
 };
-__device__ __forceinline__ Pieces pieces_of(const Walk& k) {
-  Pieces p;
-  const long long total = k.wk.total;
-  const int active = k.wk.active;
-  p.c0 = cta_of_unit(k.seg_first, total, active);
-  p.n = cta_of_unit(k.seg_first + k.sp.tiles - 1, total, active) - p.c0 + 1;
-  p.mid = range_begin(total, p.c0, active) < k.seg_first;
-  return p;
+
+// Writes down the segment that this CTA's range is the first to start inside of, if any. One thread.
+__device__ __forceinline__ void write_pieces(const Kv8AttnArgs& a, const Work& wk) {
+  Pieces p{0, 0, 0, 0};
+  if (wk.begin < wk.end && blockIdx.x > 0) {
+    Place at;
+    at.start(a, wk);
+    at.seek(a, wk.begin);
+    if (at.tile > 0 && at.tile < at.sp.tiles && range_begin(wk.total, blockIdx.x - 1, wk.active) <= at.seg_first) {
+      p.head = at.b * a.Hkv + at.h;
+      p.c0 = cta_of_unit(at.seg_first, wk.total, wk.active);
+      p.n = cta_of_unit(at.seg_first + at.sp.tiles - 1, wk.total, wk.active) - p.c0 + 1;
+      p.mid = range_begin(wk.total, p.c0, wk.active) < at.seg_first;
+    }
+  }
+  reinterpret_cast<Pieces*>(a.split)[blockIdx.x] = p;
+}
+
+// o = 0 and lse = -inf, or the earlier partial result, for the sequences without tokens. One warp, `first` of `step`
+// that share the rows: neighbouring ones go to different warps.
+template <typename T>
+__device__ __forceinline__ void empty_rows(const Kv8AttnArgs& a, int first, int step) {
+  const int lane = threadIdx.x & 31, Hq = a.Hkv * a.G;
+  const long long rows = (long long)a.B * Hq;
+  for (long long at = first; at < rows; at += 32LL * step) {
+    const long long mine = at + (long long)lane * step;
+    uint32_t todo = __ballot_sync(0xffffffffu, mine < rows && __ldg(a.lens + mine / Hq) <= 0);
+    for (; todo; todo &= todo - 1) {
+      const size_t row = at + (long long)(__ffs(todo) - 1) * step;
+      const Joined j = join_prev(a, row, -CUDART_INF_F, 0.f);
+      for (int d = lane; d < a.hd; d += 32) ((T*)a.o)[row * a.hd + d] = joined_value<T>(a, row, d, j, 0.f);
+      __syncwarp();  // lse may be lse_prev: every lane has read it
+      if (a.lse && lane == 0) a.lse[row] = j.lse;
+    }
+  }
 }
 
 // Maximum over the warp; a NaN counts only where every lane has one.

@@ -48,6 +48,7 @@ struct Kv8AttnArgs {
   float* lse;             // [B, Hq] or null
   int* err;
   int* cta_err;           // [n_cta] device error bits of each CTA, joined into *err
+  void* split;            // [n_cta] kv8::Pieces: the split segment that each CTA wrote down
   float* part;            // [2 n_cta] slots of part_stride floats: acc [G, hd], max [8], sum [8]
   int n_cta;
   int part_stride;
@@ -56,7 +57,7 @@ struct Kv8AttnPlan {
   bool tensor;            // the tensor-core kernel (bf16, head_dim 128)
   int n_cta;
   int part_stride;
-  size_t cta_err_off, part_off, ws_bytes;
+  size_t split_off, cta_err_off, part_off, ws_bytes;
 };
 Kv8AttnPlan plan_kv8_attn(const lr_kv8_pages& kv, int n_q_heads, int sm_count);
 // Tensor map of a pool of pages with head_dim 128, a box one page of one head (plan.cu).
