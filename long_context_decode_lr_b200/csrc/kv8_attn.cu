@@ -392,16 +392,16 @@ cudaError_t launch_attn_any(const Kv8AttnArgs& a, bool bf16, cudaStream_t st) {
 
 // ------------------------------------------------------------------ joining the pieces
 //
-// CTA (c, y): every gridDim.y-th query head of the segment that CTA c of the attention kernel wrote down (none,
-// most of the time). Four numbers to a thread, the pieces spread over the rest of the threads, so that all of
+// CTA (c, g): query head g of the segment that CTA c of the attention kernel wrote down (none, most of the time).
+// Four numbers to a thread, the pieces spread over the rest of the threads, so that all of
 // them are under way at once; the order of the sums is fixed by the threads. CTA (0, 0) collects the
 // device errors too.
 
 constexpr int JT = 128;
-constexpr int kMaxCtas = 1184;  // eight to an SM: as many as are there at once
+constexpr int kMaxCtas = 1024;
 
 template <typename T>
-__global__ void __launch_bounds__(JT, 7) kv8_join_kernel(Kv8AttnArgs a) {
+__global__ void __launch_bounds__(JT, 8) kv8_join_kernel(Kv8AttnArgs a) {
   __shared__ float weight[kMaxCtas], sum_of[kMaxCtas];
   __shared__ float red[2][JT / 32];
   __shared__ __align__(16) float sums[JT * 4];
@@ -423,70 +423,67 @@ __global__ void __launch_bounds__(JT, 7) kv8_join_kernel(Kv8AttnArgs a) {
   const int n = pc.n;
   if (n == 0) return;
   const int cols = hd / 4, groups = JT / cols, col = tid % cols, group = tid / cols;
-#pragma unroll 1
-  for (int g = blockIdx.y; g < a.G; g += gridDim.y) {
-    const size_t row = (size_t)pc.head * a.G + g;
-    const int ml = a.G * hd + g;
-    auto values = [&](int i) {
-      return __ldcg(reinterpret_cast<const float4*>(a.part + (size_t)pc.slot(i) * a.part_stride + g * hd) + col);
-    };
-    // a thread's first pieces are on their way before their weights are known
-    constexpr int kAhead = 10;
-    float4 v[kAhead];
+  const int g = blockIdx.y;
+  const size_t row = (size_t)pc.head * a.G + g;
+  const int ml = a.G * hd + g;
+  auto values = [&](int i) {
+    return __ldcg(reinterpret_cast<const float4*>(a.part + (size_t)pc.slot(i) * a.part_stride + g * hd) + col);
+  };
+  // a thread's first pieces are on their way before their weights are known
+  constexpr int kAhead = 8;
+  float4 v[kAhead];
 #pragma unroll
-    for (int x = 0; x < kAhead; ++x) {
-      const int i = group + x * groups;
-      v[x] = group < groups && i < n ? values(i) : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    float m = -CUDART_INF_F;
-    for (int i = tid; i < n; i += JT) {
-      const float* at = a.part + (size_t)pc.slot(i) * a.part_stride + ml;
-      const float mi = __ldcg(at);
-      sum_of[i] = __ldcg(at + 8);
-      weight[i] = mi;
-      m = fmaxf(m, mi);
-    }
-    m = warp_max(m);
-    if (lane == 0) red[0][warp] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    const float ref = m == -CUDART_INF_F ? 0.f : m;
-    float l = 0.f;
-    for (int i = tid; i < n; i += JT) {
-      const float w = exp2f(weight[i] - ref);
-      weight[i] = w;
-      l = fmaf(w, sum_of[i], l);
-    }
-    l = warp_sum(l);
-    if (lane == 0) red[1][warp] = l;
-    __syncthreads();
-    l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-    if (group < groups) {
-      float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-      auto add = [&](int i, const float4& x) {
-        const float w = weight[i];
-        s.x = fmaf(w, x.x, s.x);
-        s.y = fmaf(w, x.y, s.y);
-        s.z = fmaf(w, x.z, s.z);
-        s.w = fmaf(w, x.w, s.w);
-      };
-#pragma unroll
-      for (int x = 0; x < kAhead; ++x)
-        if (group + x * groups < n) add(group + x * groups, v[x]);
-#pragma unroll 4
-      for (int i = group + kAhead * groups; i < n; i += groups) add(i, values(i));
-      reinterpret_cast<float4*>(sums)[group * cols + col] = s;
-    }
-    const Joined j = join_prev(a, row, m, l);
-    __syncthreads();  // lse may be lse_prev: every thread has read it
-    for (int d = tid; d < hd; d += JT) {
-      float acc = 0.f;
-      for (int x = 0; x < groups; ++x) acc += sums[x * hd + d];
-      ((T*)a.o)[row * hd + d] = joined_value<T>(a, row, d, j, acc);
-    }
-    if (a.lse && tid == 0) a.lse[row] = j.lse;
-    __syncthreads();  // the next head uses the same shared memory
+  for (int x = 0; x < kAhead; ++x) {
+    const int i = group + x * groups;
+    v[x] = group < groups && i < n ? values(i) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
+  float m = -CUDART_INF_F;
+  for (int i = tid; i < n; i += JT) {
+    const float* at = a.part + (size_t)pc.slot(i) * a.part_stride + ml;
+    const float mi = __ldcg(at);
+    sum_of[i] = __ldcg(at + 8);
+    weight[i] = mi;
+    m = fmaxf(m, mi);
+  }
+  m = warp_max(m);
+  if (lane == 0) red[0][warp] = m;
+  __syncthreads();
+  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+  const float ref = m == -CUDART_INF_F ? 0.f : m;
+  float l = 0.f;
+  for (int i = tid; i < n; i += JT) {
+    const float w = exp2f(weight[i] - ref);
+    weight[i] = w;
+    l = fmaf(w, sum_of[i], l);
+  }
+  l = warp_sum(l);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+  if (group < groups) {
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+    auto add = [&](int i, const float4& x) {
+      const float w = weight[i];
+      s.x = fmaf(w, x.x, s.x);
+      s.y = fmaf(w, x.y, s.y);
+      s.z = fmaf(w, x.z, s.z);
+      s.w = fmaf(w, x.w, s.w);
+    };
+#pragma unroll
+    for (int x = 0; x < kAhead; ++x)
+      if (group + x * groups < n) add(group + x * groups, v[x]);
+#pragma unroll 4
+    for (int i = group + kAhead * groups; i < n; i += groups) add(i, values(i));
+    reinterpret_cast<float4*>(sums)[group * cols + col] = s;
+  }
+  const Joined j = join_prev(a, row, m, l);
+  __syncthreads();  // lse may be lse_prev: every thread has read it
+  for (int d = tid; d < hd; d += JT) {
+    float acc = 0.f;
+    for (int x = 0; x < groups; ++x) acc += sums[x * hd + d];
+    ((T*)a.o)[row * hd + d] = joined_value<T>(a, row, d, j, acc);
+  }
+  if (a.lse && tid == 0) a.lse[row] = j.lse;
 }
 
 template <typename T>
@@ -500,7 +497,7 @@ cudaError_t launch_attn(const Kv8AttnArgs& a, const Kv8AttnPlan& plan, cudaStrea
     e = launch_attn_any(a, sizeof(T) == 2, st);
   }
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kv8_join_kernel<T>, dim3(plan.n_cta, std::max(1, std::min(a.G, kMaxCtas / plan.n_cta))), JT, 0, st, a);
+  return launch_overlapped(kv8_join_kernel<T>, dim3(plan.n_cta, a.G), JT, 0, st, a);
 }
 
 }  // namespace
