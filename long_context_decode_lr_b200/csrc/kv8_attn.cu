@@ -13,16 +13,20 @@
 //
 // One CTA of 128 threads walks its share of the batch's tiles (kv8_common.cuh). Warp w takes the 32 tokens from
 // 32 w on of every tile, by itself: its own maximum, sum and accumulators, joined with the other warps' at the
-// segment's end. Every lane copies what it will use itself to shared memory, two tiles ahead (cp.async), so a
-// warp waits for nobody. Bound by the bytes under way; on the CUDA cores, with two multiply-adds to
-// an instruction, it was bound by instructions at a third of HBM's rate.
+// segment's end. Its rows of a page are one piece of memory each for keys and values, copied as such to shared
+// memory two tiles ahead, so a warp waits for nobody. Bound by its instructions' latency with two warps to a
+// scheduler; on the CUDA cores, with two multiply-adds to an instruction, it took a
+// quarter longer with four query heads per KV head and twice as long with eight.
 #include <algorithm>
 
 #include "kv8_common.cuh"
+#include "sm100.cuh"
 
 namespace lr {
 namespace kv8 {
 namespace {
+
+using namespace sm100;
 
 constexpr int NT = 128, kWarps = NT / 32;
 static_assert(kTileTokens == NT, "32 tokens of a tile to a warp");
@@ -43,27 +47,22 @@ __device__ __forceinline__ void split(float x, float y, uint32_t& t0, uint32_t& 
   t1 = bits(__floats2half2_rn((x - f.x) * 2048.f, (y - f.y) * 2048.f));
 }
 
-// Copies kBytes (8 or 16) of which `n` are there; the rest becomes 0. `wide`: 16-byte aligned.
-template <int kBytes>
-__device__ __forceinline__ void copy_part(uint32_t smem, const uint8_t* from, int n, bool wide) {
-  if (kBytes == 16 && wide) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem), "l"(from), "r"(n) : "memory");
+template <int kWords>
+__device__ __forceinline__ void load_words(const uint8_t* smem, bool wide, uint32_t (&w)[kWords]) {
+  if (kWords == 4 && wide) {
+    const uint4 v = *reinterpret_cast<const uint4*>(smem);
+    w[0] = v.x;
+    w[1] = v.y;
+    w[2] = v.z;
+    w[3] = v.w;
     return;
   }
 #pragma unroll
-  for (int x = 0; x < kBytes; x += 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(smem + x), "l"(n > x ? from + x : from), "r"(n > x ? 8 : 0)
-                 : "memory");
-}
-__device__ __forceinline__ uint4 load16(uint32_t smem) {
-  uint4 v;
-  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(smem) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint2 load8(uint32_t smem) {
-  uint2 v;
-  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(smem) : "memory");
-  return v;
+  for (int i = 0; i < kWords; i += 2) {
+    const uint2 v = *reinterpret_cast<const uint2*>(smem + 4 * i);
+    w[i] = v.x;
+    w[i + 1] = v.y;
+  }
 }
 
 template <int HD>
@@ -71,8 +70,8 @@ struct Ring {
   static constexpr int kStages = 3;
   static constexpr int kBatch = HD <= 128 ? 32 : 16;      // tokens of a stage
   static constexpr int kKeyParts = HD / 64;               // 16 bytes each, of a lane's quarter of a row
-  static constexpr int kValueBytes = HD == 64 ? 8 : 16;   // of a part of a lane's eighth of a row
-  static constexpr int kValueParts = HD / 8 / kValueBytes;
+  static constexpr int kValueWords = HD == 64 ? 2 : 4;    // of a part of a lane's eighth of a row
+  static constexpr int kValueParts = HD / 32 / kValueWords;
   static constexpr int kValues = kBatch * HD;             // offset of the values in a stage
   static constexpr int kStageBytes = 2 * kBatch * HD;
   static constexpr int kWarpBytes = kStages * kStageBytes;
@@ -94,16 +93,24 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
   __shared__ int err;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hi = lane >> 2, c = lane & 3;
   const int hd = a.hd, G = a.G;
-  const int value_dim = hi * (HD / 8), value_bytes = max(0, min(HD / 8, hd - value_dim));
   const bool wide = hd % 16 == 0;
-  const uint32_t my_ring = (uint32_t)__cvta_generic_to_shared(ring) + warp * R::kWarpBytes;
+  uint8_t* const my_ring = ring + warp * R::kWarpBytes;
+  __shared__ uint64_t full[kWarps][R::kStages];
+  __shared__ volatile int gave_up;
   auto sums = [&](int w, int g) { return reinterpret_cast<float*>(ring + w * R::kWarpBytes) + g * kSumStride; };
-  if (tid == 0) err = 0;
+  if (tid == 0) {
+    err = 0;
+    gave_up = 0;
+    for (int i = 0; i < kWarps * R::kStages; ++i) mbar_init(&full[0][i], 1);
+    fence_mbar_init();
+  }
   prefetch_inputs(a);
   grid_dependency();
   Walk k(a, find_work<NT>(a, scratch));
   if (blockIdx.x == 0 && k.wk.bad_len) atomicOr(&err, LR_DEVERR_LEN);
   if (tid == 0) write_pieces(a, k.wk);
+  uint32_t stages = 0;  // copied to so far, by this warp
+  bool ok = true;       // once a wait has failed the rest runs through without waiting: nobody is left at a barrier
   while (k.next()) {
     const int* table = a.table + (size_t)k.b * a.max_pages;
     const size_t row0 = ((size_t)k.b * a.Hkv + k.h) * G;
@@ -136,38 +143,26 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
         b.from = b.to = 0;
       }
     };
-    // A stage: of the keys, the rows of tokens 8 n + hi; of the values, those of tokens
-    // 16 n + {2c, 2c + 1, 2c + 8, 2c + 9}.
-    auto copy = [&](int i, const Part& b) {
-      if (b.to > b.from) {
-        const uint32_t to = my_ring + i % R::kStages * R::kStageBytes;
-        const size_t head = (size_t)b.id * a.page_stride + ((size_t)k.h * kBlock + b.row) * hd;
-        const uint8_t* keys = a.kc + head + (unsigned)(hi * hd + 16 * c);
-        const uint8_t* values = a.vc + head + (unsigned)(2 * c * hd + value_dim);
-#pragma unroll
-        for (int n = 0; n < kBatch / 8; ++n) {
-          const int t = 8 * n + hi, row_bytes = t >= b.from && t < b.to ? hd - 16 * c : 0;
-#pragma unroll
-          for (int x = 0; x < R::kKeyParts; ++x) {
-            const int bytes = max(0, min(16, row_bytes - 64 * x));
-            copy_part<16>(to + ((n * R::kKeyParts + x) * 32 + lane) * 16, bytes ? keys + (unsigned)(8 * n * hd) + 64 * x : a.kc,
-                          bytes, wide);
-          }
-        }
-#pragma unroll
-        for (int n = 0; n < kBatch / 4; ++n) {
-          const int row = n / 4 * 16 + (n & 1) + (n >> 1 & 1) * 8, t = 2 * c + row;
-          const int bytes = t >= b.from && t < b.to ? value_bytes : 0;
-#pragma unroll
-          for (int x = 0; x < R::kValueParts; ++x)
-            copy_part<R::kValueBytes>(to + R::kValues + ((n * R::kValueParts + x) * 32 + lane) * R::kValueBytes,
-                                      bytes > R::kValueBytes * x ? values + (unsigned)(row * hd) + R::kValueBytes * x : a.vc,
-                                      max(0, min(R::kValueBytes, bytes - R::kValueBytes * x)), wide);
+    const uint32_t first_stage = stages;
+    const unsigned batch_bytes = kBatch * hd;
+    auto copy = [&](const Part& b) {
+      __syncwarp();  // the stage's last batch has been read
+      if (lane == 0) {
+        const uint32_t s = stages % R::kStages;
+        uint64_t* bar = &full[warp][s];
+        if (b.to > b.from) {
+          const size_t at = (size_t)b.id * a.page_stride + ((size_t)k.h * kBlock + b.row) * hd;
+          mbar_arrive_expect_tx(bar, 2 * batch_bytes);
+          bulk_load(my_ring + s * R::kStageBytes, a.kc + at, batch_bytes, bar);
+          bulk_load(my_ring + s * R::kStageBytes + R::kValues, a.vc + at, batch_bytes, bar);
+        } else {
+          mbar_arrive(bar);
         }
       }
-      asm volatile("cp.async.commit_group;" ::: "memory");
+      ++stages;
     };
     Part now = part_of(0), next = part_of(1), after = part_of(2);
+    fence_proxy_async_smem();
     __syncthreads();  // the last segment's queries and sums have been read
 
     // head `hi` of the queries, the dims of this lane's keys: scaled to [2^14, 2^15) and split
@@ -195,9 +190,9 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
         top = fmaxf(top, fmaxf(fmaxf(fabsf(v.x), fabsf(v.y)), fmaxf(fabsf(v.z), fabsf(v.w))));
       }
       resolve(now);
-      copy(0, now);
+      copy(now);
       resolve(next);
-      copy(1, next);
+      copy(next);
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
       top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
       const int e = max((int)(__float_as_uint(top) >> 23) - 127 - 14, -112);
@@ -221,26 +216,37 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
 
     for (int i = 0; i < n_batches; ++i) {
       resolve(after);
-      copy(i + 2, after);
+      copy(after);
       const Part last = part_of(i + 3);
-      asm volatile("cp.async.wait_group 2;" ::: "memory");
-      const uint32_t stage = my_ring + i % R::kStages * R::kStageBytes;
+      const uint32_t at_stage = first_stage + i;
+      if (ok && !(ok = mbar_wait(&full[warp][at_stage % R::kStages], (at_stage / R::kStages) & 1, &gave_up))) {
+        gave_up = 1;
+        atomicOr(&err, LR_DEVERR_TIMEOUT);
+      }
+      const uint8_t* stage = my_ring + at_stage % R::kStages * R::kStageBytes;
+      const bool masked = now.from > 0 || now.to < kBatch;
       const bool any = now.to > now.from;  // else the stage holds what it held
       float x[kBatch / 8][2];  // scores of tokens 8 n + 2c and 8 n + 2c + 1
       {
         float s[kBatch / 8][4] = {};
 #pragma unroll
         for (int y = 0; y < R::kKeyParts; ++y) {
-          uint4 w[kBatch / 8];
+          uint32_t w[kBatch / 8][4];
+          const int d = 64 * y + 16 * c;
 #pragma unroll
-          for (int n = 0; n < kBatch / 8; ++n) w[n] = load16(stage + ((n * R::kKeyParts + y) * 32 + lane) * 16);
+          for (int n = 0; n < kBatch / 8; ++n) {
+            load_words(stage + (unsigned)((8 * n + hi) * hd + d), wide, w[n]);
+            if (hd < HD) {  // what is behind the row may be a NaN code
+              if (d >= hd) w[n][0] = w[n][1] = 0;
+              if (d + 8 >= hd) w[n][2] = w[n][3] = 0;
+            }
+          }
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const uint4 q = queries[4 * y + j][lane];
 #pragma unroll
             for (int n = 0; n < kBatch / 8; ++n) {
-              const uint32_t v = j == 0 ? w[n].x : j == 1 ? w[n].y : j == 2 ? w[n].z : w[n].w;
-              mma_f16(s[n], q.x, q.y, q.z, q.w, code_pair(v), code_pair(v >> 16));
+              mma_f16(s[n], q.x, q.y, q.z, q.w, code_pair(w[n][j]), code_pair(w[n][j] >> 16));
             }
           }
         }
@@ -249,7 +255,7 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
 #pragma unroll
           for (int y = 0; y < 2; ++y) x[n][y] = fmaf(s[n][2 + y], 1.f / 2048.f, s[n][y]) * (factor * now.ks);
       }
-      if (now.from > 0 || now.to < kBatch) {
+      if (masked) {
 #pragma unroll
         for (int n = 0; n < kBatch / 8; ++n)
 #pragma unroll
@@ -295,27 +301,21 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
         if (!any) continue;
 #pragma unroll
         for (int z = 0; z < R::kValueParts; ++z) {
-          uint32_t r[4][R::kValueBytes / 4];  // of the rows 2c, 2c + 1, 2c + 8 and 2c + 9
+          uint32_t r[4][R::kValueWords];  // of the rows 2c, 2c + 1, 2c + 8 and 2c + 9
 #pragma unroll
           for (int y = 0; y < 4; ++y) {
-            const uint32_t at = stage + R::kValues + (((4 * n + y) * R::kValueParts + z) * 32 + lane) * R::kValueBytes;
-            if constexpr (R::kValueBytes == 16) {
-              const uint4 v = load16(at);
-              r[y][0] = v.x;
-              r[y][1] = v.y;
-              r[y][2] = v.z;
-              r[y][3] = v.w;
-            } else {
-              const uint2 v = load8(at);
-              r[y][0] = v.x;
-              r[y][1] = v.y;
+            const int t = 16 * n + 2 * c + (y & 1) + (y >> 1) * 8;
+            load_words(stage + R::kValues + (unsigned)(t * hd + hi * (HD / 8) + 4 * R::kValueWords * z), wide, r[y]);
+            if (masked && (t < now.from || t >= now.to)) {
+#pragma unroll
+              for (int w = 0; w < R::kValueWords; ++w) r[y][w] = 0;
             }
           }
 #pragma unroll
-          for (int w = 0; w < R::kValueBytes / 4; ++w) {  // four dims: pairs of tokens
+          for (int w = 0; w < R::kValueWords; ++w) {  // four dims: pairs of tokens
             const uint32_t a0 = __byte_perm(r[0][w], r[1][w], 0x5140), a1 = __byte_perm(r[0][w], r[1][w], 0x7362);
             const uint32_t b0 = __byte_perm(r[2][w], r[3][w], 0x5140), b1 = __byte_perm(r[2][w], r[3][w], 0x7362);
-            float(*to)[4] = acc + z * R::kValueBytes + 4 * w;
+            float(*to)[4] = acc + 4 * (z * R::kValueWords + w);
             mma_f16(to[0], p[0], p[1], p[2], p[3], code_pair(a0), code_pair(b0));
             mma_f16(to[1], p[0], p[1], p[2], p[3], code_pair(a0 >> 16), code_pair(b0 >> 16));
             mma_f16(to[2], p[0], p[1], p[2], p[3], code_pair(a1), code_pair(b1));
@@ -327,6 +327,7 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
       next = after;
       after = last;
     }
+    __syncwarp();  // the ring has been read: the sums take its place
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
     if (c == 0) {
@@ -374,6 +375,9 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
       }
     }
   }
+  if (!ok)  // nothing may land in shared memory after the CTA has gone
+    for (uint32_t j = stages > R::kStages ? stages - R::kStages : 0; j < stages; ++j)
+      mbar_wait_drain(&full[warp][j % R::kStages], (j / R::kStages) & 1, kWaitCycles / 4);
   if (bf16) empty_rows<__nv_bfloat16>(a, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
   else empty_rows<float>(a, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
   __syncthreads();
@@ -420,8 +424,8 @@ __global__ void __launch_bounds__(JT, 8) kv8_join_kernel(Kv8AttnArgs a) {
   }
   const int4 said = __ldcg(reinterpret_cast<const int4*>(a.split) + blockIdx.x);
   const Pieces pc{said.x, said.y, said.z, said.w};
-  const int n = pc.n;
-  if (n == 0) return;
+  const int n = min(pc.n, min(a.n_cta - pc.c0, kMaxCtas));
+  if (n <= 0) return;
   const int cols = hd / 4, groups = JT / cols, col = tid % cols, group = tid / cols;
   const int g = blockIdx.y;
   const size_t row = (size_t)pc.head * a.G + g;

@@ -202,7 +202,8 @@ __device__ __forceinline__ int cta_of_unit(long long t, long long total, int act
   return (int)(((t + 1) * active - 1) / total);
 }
 
-// A place on the line that moves forward.
+// A place on the line that moves forward. It stays inside the batch even if somebody changes the lengths under the
+// kernel (a caller's mistake: then the result is garbage, and nothing else).
 struct Place {
   int b, h;
   Span sp;
@@ -215,12 +216,13 @@ struct Place {
     sp = seq_span(a, b);
   }
   __device__ __forceinline__ void seek(const Kv8AttnArgs& a, long long unit) {
-    while (unit >= b_first + (long long)sp.units * a.Hkv) {
+    while (unit >= b_first + (long long)sp.units * a.Hkv && b + 1 < a.B) {
       b_first += (long long)sp.units * a.Hkv;
       sp = seq_span(a, ++b);
     }
     const long long in = unit - b_first;
-    h = in <= INT_MAX ? (int)in / sp.units : (int)(in / sp.units);
+    const int units = max(1, sp.units);
+    h = min(in <= INT_MAX ? (int)in / units : (int)min(in / units, (long long)INT_MAX), a.Hkv - 1);
     seg_first = b_first + (long long)h * sp.units;
     tile = (int)(unit - seg_first);
   }
@@ -240,7 +242,7 @@ struct Walk : Place {
   __device__ bool next() {
     while (at < wk.end) {
       seek(a, at);
-      at = seg_first + sp.units;
+      at = max(at + 1, seg_first + sp.units);
       tile0 = tile;
       tile1 = (int)min((long long)sp.tiles, wk.end - seg_first);
       if (tile0 < tile1) return true;
