@@ -550,7 +550,7 @@ lr_status lr_kv8_append(const lr_kv8_pages* kv, int32_t n_q_heads, int32_t n_tok
   a.rot = rot;
   a.interleaved = rot ? rope->interleaved : 0;
   a.err = (int*)ws;
-  const cudaError_t e = lr::launch_kv8_append(a, kv->dtype, (cudaStream_t)stream);
+  const cudaError_t e = lr::launch_kv8_append(a, kv->dtype, current_sm_count(), (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "append launch");
   return LR_OK;
 }

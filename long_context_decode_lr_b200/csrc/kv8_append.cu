@@ -641,7 +641,7 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
 }
 
 template <typename T>
-cudaError_t launch_append(const Kv8AppendArgs& a, cudaStream_t st) {
+cudaError_t launch_append(const Kv8AppendArgs& a, int sm_count, cudaStream_t st) {
   if (!a.cu) {
     const long long warps = (long long)a.B * (a.Hkv + a.Hq);
     const unsigned grid = (unsigned)((warps + kOneWarps - 1) / kOneWarps) + 1;
@@ -652,9 +652,16 @@ cudaError_t launch_append(const Kv8AppendArgs& a, cudaStream_t st) {
   const int threads = kBlock * ((a.hd + 15) / 16);
   const int units = a.n_tokens / kBlock + 2 * a.B;
   const int smem = ahead<T>() * 2 * 8 * (int)sizeof(T) * threads;
-  // Heads are shared out among up to 8 CTAs. Each finds the page's angles again, but they fill the machine
-  // evenly to the end: 121 us for 32K tokens of 32 + 8 heads with 8 of them, 126 with 4, 132 with one.
-  const int ny = std::min(a.Hkv, 8);
+  // Heads are shared out among up to 8 CTAs, which fill the machine evenly to the end. Each finds the page's angles
+  // again, though, so with more pages than SMs a share has four query heads at least: 32K tokens of 32 + 8
+  // heads take 122 us with 8 shares, 127 with 4, 132 with one; of 8 + 8 heads 88, 73 and 68. Where most
+  // pages get a few tokens a share's beginning weighs more: 20 tokens each of 128 sequences 27 us
+  // with 8, 22 with 2.
+  int ny = std::min(a.Hkv, 8);
+  if (units > sm_count) {
+    ny = std::max(1, std::min(ny, a.Hq / 4));
+    if (a.n_tokens < (long long)kBlock / 2 * a.B) ny = std::min(ny, 2);
+  }
   void (*kernel)(Kv8AppendArgs, int) = kv8_append_kernel<T, Turn::kMixed>;
   if (a.hd % 16 == 0 && a.rot == 0) kernel = kv8_append_kernel<T, Turn::kNone>;
   else if (a.hd % 16 == 0 && a.rot == a.hd)
@@ -669,9 +676,9 @@ cudaError_t launch_append(const Kv8AppendArgs& a, cudaStream_t st) {
 }  // namespace
 }  // namespace kv8
 
-cudaError_t launch_kv8_append(const Kv8AppendArgs& a, lr_dtype dt, cudaStream_t st) {
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, lr_dtype dt, int sm_count, cudaStream_t st) {
   if (a.B == 0) return cudaMemsetAsync(a.err, 0, 256, st);
-  return dt == LR_BF16 ? kv8::launch_append<__nv_bfloat16>(a, st) : kv8::launch_append<float>(a, st);
+  return dt == LR_BF16 ? kv8::launch_append<__nv_bfloat16>(a, sm_count, st) : kv8::launch_append<float>(a, sm_count, st);
 }
 
 }  // namespace lr

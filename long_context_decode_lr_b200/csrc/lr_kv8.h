@@ -29,7 +29,7 @@ struct Kv8AppendArgs {
   int rot, interleaved;
   int* err;
 };
-cudaError_t launch_kv8_append(const Kv8AppendArgs& a, lr_dtype dt, cudaStream_t st);
+cudaError_t launch_kv8_append(const Kv8AppendArgs& a, lr_dtype dt, int sm_count, cudaStream_t st);
 
 struct Kv8AttnArgs {
   int B, Hkv, G, hd, n_pages, max_pages, window;
