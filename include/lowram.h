@@ -38,7 +38,8 @@
  *     r a multiple of 64 and at most 8 query heads per KV head, and lr_pack_prefill
  *     on bf16 with hd = 128, H of 128 or 256 and r a multiple of 128, run on the
  *     tensor-core kernels; other shapes run on CUDA-core kernels, with the same
- *     results to the stated tolerances. Two
+ *     results to the stated tolerances. lr_decode_attn_kv8 runs on tensor-core kernels for
+ *     every shape. Two
  *     environment variables, read at each call, force the CUDA-core kernels on
  *     shapes the tensor-core kernels would take: LOWRAM_DECODE_PATH=general (decode
  *     entry points) and LOWRAM_PACK_PATH=general (lr_pack_prefill). Any other value,
@@ -458,8 +459,8 @@ typedef struct lr_kv8_pages {
  * pair j of a token at position pos turns by the angle pos * inv_freq[j],
  *     (x0, x1) -> (x0 cos - x1 sin, x1 cos + x0 sin),
  * where pair j is dims (j, rot_dim / 2 + j), or (2j, 2j + 1) with interleaved = 1.
- * inv_freq [rot_dim / 2] fp32 in radians per token. The angle is reduced exactly: it is right to
- * about 1e-6 radians at every position an int32 can hold.
+ * inv_freq [rot_dim / 2] fp32 in radians per token. The angle is reduced exactly: sine and cosine are
+ * right to about 5e-7 at every position an int32 can hold (to fp32 rounding where dtype is LR_F32).
  */
 typedef struct lr_rope {
   const float* inv_freq;
@@ -525,6 +526,10 @@ size_t lr_kv8_attn_workspace_bytes(const lr_kv8_pages* kv, int32_t n_q_heads);
  * Inputs:  q [B, Hq, hd], Hq a multiple of Hkv with at most 8 query heads per KV head;
  *          o_prev [B, Hq, hd] and lse_prev [B, Hq] fp32, both or neither.
  * Outputs: o [B, Hq, hd]; lse [B, Hq] fp32 or NULL. o may be o_prev, lse may be lse_prev.
+ * A query head with a NaN or an infinite number gives NaN; a NaN code gives NaN where it is attended.
+ * Queries and weights enter the products as sums of narrower numbers: a bf16 query is exact down to 2^-15
+ * of its head's largest number, an fp32 one to 2^-24; weights are right to 2^-24, with LR_BF16 and
+ * head_dim 128 to 2^-12 (to 2^-28 of the largest weight of their 128 tokens where they are under 2^-16 of it).
  * Device checks: a length out of bounds is clipped to [0, 64 max_pages] (LR_DEVERR_LEN), a page id
  * out of range leaves that page's tokens out (LR_DEVERR_PAGE).
  */

@@ -5,11 +5,14 @@
 // raising it when larger numbers arrive shifts the codes' exponents and loses nothing but what
 // falls under the smallest code. Whoever writes a page therefore owns it: one CTA (or warp, with one
 // token per sequence) takes all of a call's rows of a page and head, finds their largest
-// magnitude, settles the scale and writes the codes. Bound by memory: the rows are read once and
-// stay in registers between the maximum and the rounding.
+// magnitude, settles the scale and writes the codes. The rows are read from memory once and stay on the SM
+// between the maximum and the rounding.
 //
 // Angles: a pair's frequency becomes a 64-bit fraction of a turn, so position * fraction wraps at
-// whole turns by itself and far positions lose nothing; sincospif takes the top 32 bits.
+// whole turns by itself and far positions lose nothing; sine and cosine take the top 32 bits.
+//
+// Measured (B200, 32 query and 8 KV heads of 128 bf16 numbers, all rotated): 32K tokens of one sequence
+// 122 us, 6.0 TB/s of the 738 MB read and written; one token for each of 64 sequences 3.4 us.
 #include <algorithm>
 
 #include "kv8_common.cuh"
@@ -249,7 +252,8 @@ __global__ void __launch_bounds__(32 * kOneWarps) kv8_append_one_kernel(Kv8Appen
 // pairs up. The angles depend on row and chunk alone, so a thread finds its 8 sines and cosines once and
 // uses them for every head.
 //
-// Bound by memory, if enough of it is asked for in time: a thread copies its own chunks to shared memory
+// Bound by memory (fp32, and rows with few query heads, by issue slots: a KV head costs a thread about 440
+// instructions, the angles 500, a query head 90), if enough of it is asked for in time: a thread copies its own chunks to shared memory
 // with cp.async, kAhead heads ahead (query heads first, then a key and a value row per KV head), and reads
 // them back without a barrier. Keys and values meet at one barrier per KV head, for the largest magnitude.
 // That maximum is taken without a look at what is infinite (NaN drops out by itself); only a page where it

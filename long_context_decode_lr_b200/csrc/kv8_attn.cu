@@ -15,8 +15,11 @@
 // 32 w on of every tile, by itself: its own maximum, sum and accumulators, joined with the other warps' at the
 // segment's end. Its rows of a page are one piece of memory each for keys and values, copied as such to shared
 // memory two tiles ahead, so a warp waits for nobody. Bound by its instructions' latency with two warps to a
-// scheduler; on the CUDA cores, with two multiply-adds to an instruction, it took a
-// quarter longer with four query heads per KV head and twice as long with eight.
+// scheduler (about 900 instructions for a warp's 8 KB).
+//
+// Measured (B200, 60000 tokens of one sequence, 8 KV heads): fp32, head_dim 128, 36.5 us with 4 query heads per KV
+// head, 38 with 8 (3.4 TB/s; on the CUDA cores, two multiply-adds to an instruction, 60 and 103); head_dim 64
+// 25; bf16, head_dim 256, four sequences of 30000 tokens 114 us (4.3 TB/s).
 #include <algorithm>
 
 #include "kv8_common.cuh"

@@ -17,8 +17,14 @@
 // (one per head and tile, a warp reduction and four numbers in shared memory) is the only thing the
 // threads exchange. Scales and the rescaling between tiles are fp32 factors in registers.
 //
-// Persistent, two CTAs per SM on an even share of the tiles (kv8_common.cuh): warps 0-3 softmax and
-// sums, warp 4 loads (TMA, three stages of 32 KB), warp 5 issues the products. Bound by HBM: 256 bytes per token and KV head against about 2 cycles of the tensor pipe.
+// Persistent, two CTAs per SM on an even share of the tiles (kv8_common.cuh): one warp loads (TMA, three stages of
+// 32 KB), one issues the products, four or eight do softmax and sums, four for every four query heads. Scores
+// are a tile ahead of the softmax, value products a tile behind. Bound by HBM: 256 bytes per token and
+// KV head, 12 cycles of an SM's share of the bandwidth, against 2 of shared memory into the tensor pipe.
+//
+// Measured (B200, 8 KV heads of 4 query heads): four sequences of 131072 tokens 169 us, 6.3 TB/s of codes; one of
+// 262144 88 us; one of 32768 21 us, of which 5 us pass before the first tile is there and 5 us after the
+// last. The loads run at 7.3 TB/s once they have begun; SMs of the larger GPCs end up to 10 % later.
 #include <algorithm>
 
 #include "kv8_common.cuh"
@@ -121,7 +127,7 @@ __device__ __forceinline__ void give_up(const Shared& sh) {
   atomicOr(sh.err(), LR_DEVERR_TIMEOUT);
 }
 
-// ------------------------------------------------------------------ loads (warp 4)
+// ------------------------------------------------------------------ loads (one warp)
 //
 // The CTA's units are taken 16 at a time: lanes 2j and 2j + 1 find the segment of unit j and have the ids
 // and scales of its two pages, and lane 2j issues the loads of the tile. While one batch is loaded the ids
@@ -241,7 +247,7 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
   }
 }
 
-// ------------------------------------------------------------------ products (warp 5)
+// ------------------------------------------------------------------ products (one warp)
 
 // The query heads, bf16 rows of 256 bytes at q, become two e4m3 terms each, rows g and 8 + g of the K-major
 // operand in their place, and the factors that scores are multiplied by. A head with an infinite
@@ -346,7 +352,7 @@ __device__ void issue_products(const Kv8AttnArgs& a, const Shared& sh, uint32_t 
   }
 }
 
-// ------------------------------------------------------------------ softmax and sums (warps 0-3)
+// ------------------------------------------------------------------ softmax and sums (four or eight warps)
 
 template <int GROUPS>
 __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {

@@ -319,55 +319,55 @@ class Kv8Pages:
                               _ptr(k_scale), _ptr(v_scale), _ptr(page_table), _ptr(lens))
         self.ref = ctypes.byref(self.c)
 
-    # These run on every call of a decode step: plain comparisons of a tensor's type, device index and shape.
-    def _rows(self, t, n_rows, n_heads, name):
-        """Address of a [n_rows, n_heads, hd] tensor of the cache's dtype and device, and its strides."""
-        if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != (n_rows, n_heads, self.head_dim):
-            raise ValueError(f"{name} must be a {self.dtype} tensor [{n_rows}, {n_heads}, {self.head_dim}] on {self.device}")
-        return t.data_ptr() or None, t.stride()
-
+    # These run on every call of a decode step: plain comparisons of a tensor's type, device index, shape and strides.
     def _dense_rows(self, t, n_rows, n_heads, name):
-        ptr = self._rows(t, n_rows, n_heads, name)[0]
+        """Address of a dense [n_rows, n_heads, hd] tensor of the cache's dtype and device."""
+        if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != (n_rows, n_heads, self.head_dim):
+            raise self._wrong_rows(n_rows, n_heads, name)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
-        return ptr
+        return t.data_ptr() or None
 
     def _token_rows(self, t, n_rows, n_heads, name):
         """(address, elements from one token to the next, 0 for one token): the rows of a token are dense."""
-        ptr, (token, head, dim) = self._rows(t, n_rows, n_heads, name)
-        if self.head_dim > 1 and dim != 1 or n_heads > 1 and head != self.head_dim:
+        hd = self.head_dim
+        if t.dtype is not self.dtype or t.get_device() != self._index or t.shape != (n_rows, n_heads, hd):
+            raise self._wrong_rows(n_rows, n_heads, name)
+        token, head, dim = t.stride()
+        if hd > 1 and dim != 1 or n_heads > 1 and head != hd:
             raise ValueError(f"{name}: the heads of a token must be contiguous")
         if n_rows < 2:
-            return ptr, 0
-        if token < n_heads * self.head_dim:
+            token = 0
+        elif token < n_heads * hd:
             raise ValueError(f"{name}: the rows of two tokens must not overlap")
-        return ptr, token
+        return t.data_ptr() or None, token
+
+    def _wrong_rows(self, n_rows, n_heads, name):
+        return ValueError(f"{name} must be a {self.dtype} tensor [{n_rows}, {n_heads}, {self.head_dim}] on {self.device}")
 
     def _beside(self, t, dtype, shape, name):
-        if t is None:
-            return None
         if t.dtype is not dtype or t.get_device() != self._index or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on {self.device}")
         return t.data_ptr() or None
 
     def _call(self, entry, args, ws, stream):
         """Run an entry point on the cache's device, on its current stream unless one is given."""
-        if ws is None:
-            tail = (None, 0)
+        ptr = size = None
+        if ws is not None:
+            if ws.get_device() != self._index or not ws.is_contiguous():
+                raise ValueError(f"the workspace must be contiguous and live on {self.device}")
+            ptr, size = ws.data_ptr() or None, ws.nbytes
+        if stream is None:
+            stream = torch._C._cuda_getCurrentRawStream(self._index) or None
         else:
-            if ws.get_device() != self._index:
-                raise ValueError(f"the workspace must live on {self.device}")
-            tail = (_ptr(ws), ws.numel() * ws.element_size())
+            stream = getattr(stream, "cuda_stream", stream) or None
         if torch.cuda.current_device() == self._index:
-            _check(entry(*args, *tail, self._stream(stream)))
+            status = entry(*args, ptr, size or 0, stream)
         else:
             with torch.cuda.device(self.device):
-                _check(entry(*args, *tail, self._stream(stream)))
-
-    def _stream(self, stream):
-        if stream is None:
-            return torch._C._cuda_getCurrentRawStream(self._index) or None
-        return getattr(stream, "cuda_stream", stream) or None
+                status = entry(*args, ptr, size or 0, stream)
+        if status:
+            _check(status)
 
 
 class Rope:
@@ -403,7 +403,7 @@ def lr_kv8_append(kv: Kv8Pages, k, v, ws, cu_tokens=None, rope: Optional[Rope] =
         out_ptr = kv._dense_rows(q_out, n, hq, "q_out")
     if rope is not None and rope.index != kv._index:
         raise ValueError(f"inv_freq must live on {kv.device}")
-    cu = kv._beside(cu_tokens, torch.int32, (kv.batch + 1,), "cu_tokens")
+    cu = None if cu_tokens is None else kv._beside(cu_tokens, torch.int32, (kv.batch + 1,), "cu_tokens")
     kv._call(library().lr_kv8_append,
              (kv.ref, hq, n, cu, None if rope is None else rope.ref, q_ptr, q_stride, k_ptr, k_stride, v_ptr, v_stride,
               out_ptr), ws, stream)
@@ -423,8 +423,8 @@ def lr_decode_attn_kv8(kv: Kv8Pages, n_q_heads, q, o, ws, lse=None, window=0, sc
     b, shape = kv.batch, (kv.batch, n_q_heads)
     args = (kv.ref, n_q_heads, kv._dense_rows(q, b, n_q_heads, "q"), int(window), float(scale),
             None if o_prev is None else kv._dense_rows(o_prev, b, n_q_heads, "o_prev"),
-            kv._beside(lse_prev, torch.float32, shape, "lse_prev"),
-            kv._dense_rows(o, b, n_q_heads, "o"), kv._beside(lse, torch.float32, shape, "lse"))
+            None if lse_prev is None else kv._beside(lse_prev, torch.float32, shape, "lse_prev"),
+            kv._dense_rows(o, b, n_q_heads, "o"), None if lse is None else kv._beside(lse, torch.float32, shape, "lse"))
     kv._call(library().lr_decode_attn_kv8, args, ws, stream)
 
 
