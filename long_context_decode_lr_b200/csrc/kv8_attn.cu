@@ -107,6 +107,7 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
     for (int i = 0; i < kWarps * R::kStages; ++i) mbar_init(&full[0][i], 1);
     fence_mbar_init();
   }
+  __syncthreads();
   prefetch_inputs(a);
   grid_dependency();
   Walk k(a, find_work<NT>(a, scratch));
@@ -357,11 +358,11 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
         f[w] = exp2f(ml[w][0][g] - ref);
         sum = fmaf(ml[w][1][g], f[w], sum);
       }
-      Joined j{0.f, 0.f, 0.f};
+      Joined j{0.f, 0.f, 0.f, 0.f};
       if (whole) {
         j = join_prev(a, row0 + g, top, sum);
         __syncwarp();  // lse may be lse_prev: every lane has read it
-        if (a.lse && lane == 0) a.lse[row0 + g] = j.lse;
+        if (a.lse && lane == 0) a.lse[row0 + g] = j.lse();
       } else if (lane == 0) {
         slot[G * hd + g] = top;
         slot[G * hd + 8 + g] = sum;
@@ -444,29 +445,39 @@ __global__ void __launch_bounds__(JT, 8) kv8_join_kernel(Kv8AttnArgs a) {
     const int i = group + x * groups;
     v[x] = group < groups && i < n ? values(i) : make_float4(0.f, 0.f, 0.f, 0.f);
   }
-  float m = -CUDART_INF_F;
-  for (int i = tid; i < n; i += JT) {
-    const float* at = a.part + (size_t)pc.slot(i) * a.part_stride + ml;
-    const float mi = __ldcg(at);
-    sum_of[i] = __ldcg(at + 8);
-    weight[i] = mi;
-    m = fmaxf(m, mi);
+  const float prev = prev_lse(a, row);
+  float m = -CUDART_INF_F, l = 0.f;
+  if (n <= 32) {  // every warp weighs all pieces, a lane for each
+    const float* at = a.part + (size_t)pc.slot(min(lane, n - 1)) * a.part_stride + ml;
+    const float mi = lane < n ? __ldcg(at) : -CUDART_INF_F, li = lane < n ? __ldcg(at + 8) : 0.f;
+    m = warp_max(mi);
+    const float w = exp2_ftz(mi - (m == -CUDART_INF_F ? 0.f : m));
+    l = warp_sum(w * li);
+    if (warp == 0 && lane < n) weight[lane] = w;
+    __syncthreads();
+  } else {
+    for (int i = tid; i < n; i += JT) {
+      const float* at = a.part + (size_t)pc.slot(i) * a.part_stride + ml;
+      const float mi = __ldcg(at);
+      sum_of[i] = __ldcg(at + 8);
+      weight[i] = mi;
+      m = fmaxf(m, mi);
+    }
+    m = warp_max(m);
+    if (lane == 0) red[0][warp] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    const float ref = m == -CUDART_INF_F ? 0.f : m;
+    for (int i = tid; i < n; i += JT) {
+      const float w = exp2_ftz(weight[i] - ref);
+      weight[i] = w;
+      l = fmaf(w, sum_of[i], l);
+    }
+    l = warp_sum(l);
+    if (lane == 0) red[1][warp] = l;
+    __syncthreads();
+    l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
   }
-  m = warp_max(m);
-  if (lane == 0) red[0][warp] = m;
-  __syncthreads();
-  m = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-  const float ref = m == -CUDART_INF_F ? 0.f : m;
-  float l = 0.f;
-  for (int i = tid; i < n; i += JT) {
-    const float w = exp2f(weight[i] - ref);
-    weight[i] = w;
-    l = fmaf(w, sum_of[i], l);
-  }
-  l = warp_sum(l);
-  if (lane == 0) red[1][warp] = l;
-  __syncthreads();
-  l = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
   if (group < groups) {
     float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
     auto add = [&](int i, const float4& x) {
@@ -483,14 +494,14 @@ __global__ void __launch_bounds__(JT, 8) kv8_join_kernel(Kv8AttnArgs a) {
     for (int i = group + kAhead * groups; i < n; i += groups) add(i, values(i));
     reinterpret_cast<float4*>(sums)[group * cols + col] = s;
   }
-  const Joined j = join_prev(a, row, m, l);
-  __syncthreads();  // lse may be lse_prev: every thread has read it
+  const Joined j = join_with(m, l, prev);
+  __syncthreads();  // lse may be lse_prev, too: every thread has read it
   for (int d = tid; d < hd; d += JT) {
     float acc = 0.f;
     for (int x = 0; x < groups; ++x) acc += sums[x * hd + d];
     ((T*)a.o)[row * hd + d] = joined_value<T>(a, row, d, j, acc);
   }
-  if (a.lse && tid == 0) a.lse[row] = j.lse;
+  if (a.lse && tid == 0) a.lse[row] = j.lse();
 }
 
 template <typename T>

@@ -519,7 +519,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
         slot[a.G * kHd + 8 + g0 + tid] = sum;
       }
     } else {
-      Joined j{0.f, 0.f, 0.f};
+      Joined j{0.f, 0.f, 0.f, 0.f};
       if (mine < G) j = join_prev(a, row0 + mine, top, sum);
       if (a.lse_prev) soft_sync(group);  // it may be lse: every warp has read it
 #pragma unroll
@@ -527,7 +527,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
         const float inv = __shfl_sync(0xffffffffu, j.inv, g), w = __shfl_sync(0xffffffffu, j.w_prev, g);
         if (g < G) ((__nv_bfloat16*)a.o)[(row0 + g) * kHd + tid] = from_f32<__nv_bfloat16>(join_value(acc[g], inv, prev[g], w));
       }
-      if (a.lse && tid < G) a.lse[row0 + tid] = j.lse;
+      if (a.lse && tid < G) a.lse[row0 + tid] = j.lse();
     }
   }
 }
@@ -573,12 +573,13 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
     tmem_relinquish();
   }
   tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   prefetch_inputs(a);
   grid_dependency();
   const Work wk = find_work<threads_of(GROUPS)>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
   if (blockIdx.x == 0 && wk.bad_len) atomicOr(sh.err(), LR_DEVERR_LEN);
-  tc_fence_after();
-  const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   if (warp < kLoads) {
     attend<GROUPS>(a, sh, tmem);
   } else if (warp == kLoads) {

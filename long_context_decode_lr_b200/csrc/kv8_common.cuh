@@ -105,15 +105,16 @@ struct Span {
   int units;        // its stretch of the line
 };
 
-__device__ __forceinline__ Span seq_span(const Kv8AttnArgs& a, int b) {
+__device__ __forceinline__ Span span_of(const Kv8AttnArgs& a, int len) {
   Span s;
-  s.n = min(max(__ldg(a.lens + b), 0), a.max_pages * kBlock);
+  s.n = min(max(len, 0), a.max_pages * kBlock);
   s.lo = a.window > 0 ? max(0, s.n - a.window) : 0;
   s.page0 = s.lo / kBlock;
   s.tiles = s.n == 0 ? 0 : ((s.n + kBlock - 1) / kBlock - s.page0 + kTilePages - 1) / kTilePages;
   s.units = s.n == 0 ? 0 : s.tiles + kSegmentUnits;
   return s;
 }
+__device__ __forceinline__ Span seq_span(const Kv8AttnArgs& a, int b) { return span_of(a, __ldg(a.lens + b)); }
 
 // First unit of CTA c's range.
 __device__ __forceinline__ long long range_begin(long long total, int c, int active) {
@@ -141,10 +142,32 @@ struct Work {
   bool bad_len;          // this thread has seen a length out of bounds
 };
 
-// Called by all NT threads of the CTA; `scratch` holds NT + 4 long longs of shared memory.
+// Called by all NT threads of the CTA; `scratch` holds NT + 4 long longs of shared memory. Up to 32 sequences
+// are a warp's own business, a lane for each, without a barrier.
 template <int NT>
 __device__ __forceinline__ Work find_work(const Kv8AttnArgs& a, long long* scratch) {
   const int tid = threadIdx.x;
+  if (a.B <= 32) {
+    const int lane = tid & 31, len = lane < a.B ? __ldg(a.lens + lane) : 0;
+    Work wk;
+    wk.bad_len = len < 0 || len > a.max_pages * kBlock;
+    const long long mine = lane < a.B ? (long long)span_of(a, len).units * a.Hkv : 0;
+    long long run = mine;
+    for (int o = 1; o < a.B; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, run, o);
+      if (lane >= o) run += y;
+    }
+    wk.total = __shfl_sync(0xffffffffu, run, a.B - 1);
+    wk.active = (int)min((long long)a.n_cta, wk.total);
+    const int c = blockIdx.x;
+    const bool has = c < wk.active;
+    wk.begin = has ? range_begin(wk.total, c, wk.active) : 0;
+    wk.end = has ? range_begin(wk.total, c + 1, wk.active) : 0;
+    const uint32_t hit = __ballot_sync(0xffffffffu, has && wk.begin >= run - mine && wk.begin < run);
+    wk.b = max(0, __ffs(hit) - 1);
+    wk.b_first = __shfl_sync(0xffffffffu, run - mine, wk.b);
+    return wk;
+  }
   const int per = (a.B + NT - 1) / NT, b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
   long long mine = 0;
   Work wk;
@@ -256,26 +279,32 @@ struct Walk : Place {
 // the earlier partial result where there is one.
 struct Joined {
   float inv, w_prev;  // o = acc * inv + o_prev * w_prev
-  float lse;
+  float top, sum;     // lse = ln 2 (top + log2 sum)
+  __device__ __forceinline__ float lse() const {
+    return sum == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(sum));
+  }
 };
-__device__ __forceinline__ Joined join_prev(const Kv8AttnArgs& a, size_t row, float m, float l) {
+// `prev`: the earlier part's lse, -inf for none.
+__device__ __forceinline__ Joined join_with(float m, float l, float prev) {
   Joined j;
-  const float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-  const float lp = a.lse_prev ? a.lse_prev[row] * kLog2e : -CUDART_INF_F;
+  const float lp = prev * 1.4426950408889634f;
   const float own = l > 0.f || l != l ? m : -CUDART_INF_F;
-  const float top = fmaxf(own, lp);
-  if (top == -CUDART_INF_F && l == l && lp == lp) {
-    j.inv = j.w_prev = 0.f;
-    j.lse = -CUDART_INF_F;
+  j.top = fmaxf(own, lp);
+  if (j.top == -CUDART_INF_F && l == l && lp == lp) {
+    j.inv = j.w_prev = j.sum = 0.f;
     return j;
   }
-  const float w = own == -CUDART_INF_F ? 0.f : exp2f(m - top);
-  const float wp = lp == -CUDART_INF_F ? 0.f : exp2f(lp - top);
-  const float sum = fmaf(l, w, wp);
-  j.inv = w / sum;
-  j.w_prev = wp / sum;  // NaN where the sum is, with or without an earlier part
-  j.lse = kLn2 * (top + log2f(sum));
+  const float w = own == -CUDART_INF_F ? 0.f : exp2f(m - j.top);
+  const float wp = lp == -CUDART_INF_F ? 0.f : exp2f(lp - j.top);
+  j.sum = fmaf(l, w, wp);
+  const float r = __frcp_rn(j.sum);
+  j.inv = w * r;
+  j.w_prev = wp * r;  // NaN where the sum is, with or without an earlier part
   return j;
+}
+__device__ __forceinline__ float prev_lse(const Kv8AttnArgs& a, size_t row) { return a.lse_prev ? a.lse_prev[row] : -CUDART_INF_F; }
+__device__ __forceinline__ Joined join_prev(const Kv8AttnArgs& a, size_t row, float m, float l) {
+  return join_with(m, l, prev_lse(a, row));
 }
 // acc * inv + prev * w; what a weight of 0 goes with is left out, whatever it is.
 __device__ __forceinline__ float join_value(float acc, float inv, float prev, float w) {
@@ -333,7 +362,7 @@ __device__ __forceinline__ void empty_rows(const Kv8AttnArgs& a, int first, int 
       const Joined j = join_prev(a, row, -CUDART_INF_F, 0.f);
       for (int d = lane; d < a.hd; d += 32) ((T*)a.o)[row * a.hd + d] = joined_value<T>(a, row, d, j, 0.f);
       __syncwarp();  // lse may be lse_prev: every lane has read it
-      if (a.lse && lane == 0) a.lse[row] = j.lse;
+      if (a.lse && lane == 0) a.lse[row] = j.lse();
     }
   }
 }
