@@ -588,6 +588,7 @@ lr_status lr_decode_attn_kv8(const lr_kv8_pages* kv, int32_t n_q_heads, const vo
   a.part = (float*)((char*)ws + plan.part_off);
   a.n_cta = plan.n_cta;
   a.part_stride = plan.part_stride;
+  a.cluster = plan.cluster;
   const cudaError_t e = lr::launch_kv8_attn(a, plan, kv->dtype, (cudaStream_t)stream);
   if (e != cudaSuccess) return cuda_fail(e, "8-bit cache attention launch");
   return LR_OK;

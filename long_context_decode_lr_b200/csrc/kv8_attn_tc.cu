@@ -538,6 +538,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   extern __shared__ __align__(1024) uint8_t smem[];
   if (smem_u32(smem) & 1023u) {
     if (threadIdx.x == 0) {
+      if (a.cluster && blockIdx.x == 0) *a.err = LR_DEVERR_LAUNCH;
       a.cta_err[blockIdx.x] = LR_DEVERR_LAUNCH;
       reinterpret_cast<Pieces*>(a.split)[blockIdx.x] = Pieces{0, 0, 0, 0};
     }
@@ -578,13 +579,18 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   prefetch_inputs(a);
   grid_dependency();
-  const Work wk = find_work<threads_of(GROUPS)>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
+  const Work wk = a.cluster ? small_work(a) : find_work<threads_of(GROUPS)>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
   if (blockIdx.x == 0 && wk.bad_len) atomicOr(sh.err(), LR_DEVERR_LEN);
   if (warp < kLoads) {
     attend<GROUPS>(a, sh, tmem);
   } else if (warp == kLoads) {
     load_tiles(a, sh, &mk, &mv, wk);
-    if (lane == 0) write_pieces(a, wk);
+    if (a.cluster) {
+      const int bits = blockIdx.x == 0 ? check_all(a) : 0;
+      if (lane == 0 && bits) atomicOr(sh.err(), bits);
+    } else if (lane == 0) {
+      write_pieces(a, wk);
+    }
     __syncwarp();
     empty_rows<__nv_bfloat16>(a, blockIdx.x, gridDim.x);
   } else {
@@ -595,14 +601,15 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   __syncthreads();
   tc_fence_after();
   if (warp == kIssue) tmem_dealloc(tmem, tmem_cols<GROUPS>());
-  if (threadIdx.x == 0) a.cta_err[blockIdx.x] = *sh.err();
+  if (a.cluster) finish_small<__nv_bfloat16>(a, wk.pieces, *sh.err());
+  else if (threadIdx.x == 0) a.cta_err[blockIdx.x] = *sh.err();
 }
 
 template <int GROUPS>
 cudaError_t launch(const Kv8AttnArgs& a, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
   const cudaError_t e = cudaFuncSetAttribute(kv8_attn_tc_kernel<GROUPS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Layout::kBytes);
   if (e != cudaSuccess) return e;
-  return launch_overlapped(kv8_attn_tc_kernel<GROUPS>, dim3(a.n_cta), threads_of(GROUPS), Layout::kBytes, st, mk, mv, a);
+  return launch_overlapped(kv8_attn_tc_kernel<GROUPS>, dim3(a.n_cta), a.cluster, threads_of(GROUPS), Layout::kBytes, st, mk, mv, a);
 }
 
 }  // namespace

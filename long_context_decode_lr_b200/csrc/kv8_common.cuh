@@ -9,6 +9,7 @@
 
 #include "lr_common.cuh"
 #include "lr_kv8.h"
+#include "sm100.cuh"
 
 namespace lr {
 namespace kv8 {
@@ -60,17 +61,21 @@ __device__ __forceinline__ void grid_dependency() {
 // Launches a kernel that may start while the grid before drains: it waits for that grid (grid_dependency)
 // before it reads what the grid writes.
 template <typename... P, typename... A>
-cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, A&&... args) {
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+cudaError_t launch_overlapped(void (*kernel)(P...), dim3 grid, int cluster, int threads, size_t smem, cudaStream_t st,
+                              A&&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
@@ -140,6 +145,7 @@ struct Work {
   int b;                 // sequence of the first unit
   long long b_first;     // first unit of that sequence
   bool bad_len;          // this thread has seen a length out of bounds
+  int pieces;            // small calls: CTAs of the cluster that have tiles
 };
 
 // Called by all NT threads of the CTA; `scratch` holds NT + 4 long longs of shared memory. Up to 32 sequences
@@ -216,6 +222,34 @@ __device__ __forceinline__ Work find_work(const Kv8AttnArgs& a, long long* scrat
   wk.b = has ? (int)scratch[NT] : 0;
   wk.b_first = has ? scratch[NT + 1] : 0;
   return wk;
+}
+
+// Small calls: a cluster has a segment to itself, its CTAs the tiles in order, as many each as they take. The line
+// is that of the segment's sequence.
+__device__ __forceinline__ Work small_work(const Kv8AttnArgs& a) {
+  const int seg = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
+  Work wk{};
+  wk.b = seg / a.Hkv;
+  const Span sp = seq_span(a, wk.b);
+  if (sp.tiles == 0) return wk;
+  const int per = (sp.tiles + a.cluster - 1) / a.cluster, first = seg % a.Hkv * sp.units;
+  wk.pieces = (sp.tiles + per - 1) / per;
+  wk.begin = first + min(rank * per, sp.tiles);
+  wk.end = first + min((rank + 1) * per, sp.tiles);
+  return wk;
+}
+
+// Small calls: the device checks of every length and attended page, by one warp of one CTA; the bits are in every lane.
+__device__ __forceinline__ int check_all(const Kv8AttnArgs& a) {
+  int bits = 0;
+  for (int b = 0; b < a.B; ++b) {
+    const int len = __ldg(a.lens + b);
+    if (len < 0 || len > a.max_pages * kBlock) bits |= LR_DEVERR_LEN;
+    const Span sp = span_of(a, len);
+    for (int p = sp.page0 + (int)(threadIdx.x & 31); p * kBlock < sp.n; p += 32)
+      if ((unsigned)__ldg(a.table + (size_t)b * a.max_pages + p) >= (unsigned)a.n_pages) bits |= LR_DEVERR_PAGE;
+  }
+  return __reduce_or_sync(0xffffffffu, bits);
 }
 
 // The CTA whose range holds unit t, for total units over `active` CTAs: largest c with
@@ -376,6 +410,66 @@ __device__ __forceinline__ float warp_max(float v) {
 __device__ __forceinline__ float warp_sum(float v) {
   for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
   return v;
+}
+
+// Small calls: one warp joins the pieces of query head g of the cluster's segment, at most 8 of them.
+template <typename T>
+__device__ __forceinline__ void warp_join(const Kv8AttnArgs& a, int n, int g) {
+  const int lane = threadIdx.x & 31, seg = blockIdx.x / a.cluster, cols = a.hd / 4;
+  const size_t row = (size_t)seg * a.G + g, stride = 2 * (size_t)a.part_stride;
+  const float* part = a.part + (size_t)seg * a.cluster * stride;
+  const float* ml = part + (size_t)min(lane, n - 1) * stride + a.G * a.hd + g;
+  const float mi = lane < n ? __ldcg(ml) : -CUDART_INF_F, li = lane < n ? __ldcg(ml + 8) : 0.f;
+  const float prev = prev_lse(a, row);
+  Joined j;
+  float w = 0.f;
+  for (int c0 = 0; c0 < cols; c0 += 32) {
+    const int col = c0 + lane;
+    float4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      v[i] = i < n && col < cols ? __ldcg(reinterpret_cast<const float4*>(part + i * stride + g * a.hd) + col)
+                                 : make_float4(0.f, 0.f, 0.f, 0.f);
+    if (c0 == 0) {
+      const float m = warp_max(mi);
+      w = exp2_ftz(mi - (m == -CUDART_INF_F ? 0.f : m));
+      j = join_with(m, warp_sum(w * li), prev);
+    }
+    float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, w, i);
+      s.x = fmaf(wi, v[i].x, s.x);
+      s.y = fmaf(wi, v[i].y, s.y);
+      s.z = fmaf(wi, v[i].z, s.z);
+      s.w = fmaf(wi, v[i].w, s.w);
+    }
+    if (col < cols) {
+      T* o = (T*)a.o + row * a.hd + 4 * col;
+      o[0] = joined_value<T>(a, row, 4 * col, j, s.x);
+      o[1] = joined_value<T>(a, row, 4 * col + 1, j, s.y);
+      o[2] = joined_value<T>(a, row, 4 * col + 2, j, s.z);
+      o[3] = joined_value<T>(a, row, 4 * col + 3, j, s.w);
+    }
+  }
+  __syncwarp();  // lse may be lse_prev: every lane has read it
+  if (a.lse && lane == 0) a.lse[row] = j.lse();
+}
+
+// Small calls: the end of a CTA, all of its threads. The pieces are in place when the cluster has met. `bits`: its
+// device error bits, of CTA 0 those of check_all too: that CTA writes the word, which nobody has to clear; a
+// wait of another that ran out, seconds later, is added to it.
+template <typename T>
+__device__ __forceinline__ void finish_small(const Kv8AttnArgs& a, int pieces, int bits) {
+  if (threadIdx.x == 0) {
+    if (blockIdx.x == 0) *a.err = bits;
+    else if (bits & LR_DEVERR_TIMEOUT) atomicOr(a.err, LR_DEVERR_TIMEOUT);
+  }
+  __syncwarp();  // the cluster barrier is warp-aligned
+  if (a.cluster > 1) sm100::cluster_sync();
+  if (pieces < 2) return;
+  const int warps = blockDim.x / 32;
+  for (int g = blockIdx.x % a.cluster * warps + (int)threadIdx.x / 32; g < a.G; g += a.cluster * warps) warp_join<T>(a, pieces, g);
 }
 
 }  // namespace kv8

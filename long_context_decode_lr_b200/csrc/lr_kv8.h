@@ -52,9 +52,11 @@ struct Kv8AttnArgs {
   float* part;            // [2 n_cta] slots of part_stride floats: acc [G, hd], max [8], sum [8]
   int n_cta;
   int part_stride;
+  int cluster;            // 0, or CTAs of a cluster that has a segment to itself and joins it (small calls)
 };
 struct Kv8AttnPlan {
-  bool tensor;            // the tensor-core kernel (bf16, head_dim 128)
+  bool tensor;            // the tcgen05 kernel (bf16, head_dim 128)
+  int cluster;
   int n_cta;
   int part_stride;
   size_t split_off, cta_err_off, part_off, ws_bytes;

@@ -349,17 +349,26 @@ ATTN = {
     "bf16_hd72": dict(lens=[129, 64, 63], hkv=2, G=1, hd=72),
     "more_sequences_than_threads": dict(lens=[(7 * i) % 5 for i in range(700)], hkv=1, G=2),
     "more_sequences_than_threads_f32": dict(lens=[(7 * i) % 5 for i in range(300)], hkv=1, G=2, hd=64, dtype="f32"),
+    "cluster_of_8_rests": dict(lens=[1100, 130, 1, 0, 900], hkv=2, G=4),
+    "cluster_of_8_window": dict(lens=[4000, 2500], hkv=2, G=8, window=900, prev=True),
+    "cluster_of_2": dict(lens=[1000 - 61 * i for i in range(16)], hkv=8, G=4),
+    "cluster_of_1": dict(lens=[1 + 3 * i for i in range(150)], hkv=1, G=5, prev=True),
+    "cluster_of_8_f32": dict(lens=[2000, 0, 257], hkv=1, G=8, hd=256, dtype="f32", prev=True),
+    "cluster_of_4_bf16_hd72": dict(lens=[600, 64, 1, 0] * 4, hkv=4, G=3, hd=72, window=300),
     "short_segments_gqa8": dict(lens=[1 + i % 130 for i in range(90)], hkv=8, G=8),
     "bf16_hd256": dict(lens=[100, 64], hkv=2, G=4, hd=256),
 }
 
 
+@pytest.mark.parametrize("width", [None, 600], ids=["", "room_for_more"])
 @pytest.mark.parametrize("name", list(ATTN))
-def test_attention(name):
+def test_attention(name, width):
+    """`width`: page table entries of a sequence. With no more than the tokens need most of these cases are small
+    calls, which a cluster answers by itself; with room for 38400 tokens they are not."""
     c = ATTN[name]
     hd, dtype, win = c.get("hd", 128), c.get("dtype", "bf16"), c.get("window", 0)
     rng = np.random.default_rng(len(name))
-    pool = Pool(rng, c["lens"], c["hkv"], hd, dtype)
+    pool = Pool(rng, c["lens"], c["hkv"], hd, dtype, width=width)
     B, hq = len(c["lens"]), c["hkv"] * c["G"]
     q, qr = rounded(rng.standard_normal((B, hq, hd)) * 1.5, dtype)
     prev = prev_ref = None
@@ -495,10 +504,11 @@ def test_attention_nan_stays_in_its_sequence():
     assert bad[2, 4:, 9].all() and bad.sum() == 4 * 128 + 4 and np.isfinite(lse[2]).all()
 
 
-def test_attention_bad_data_is_reported_and_left_out():
+@pytest.mark.parametrize("width", [None, 600], ids=["", "room_for_more"])
+def test_attention_bad_data_is_reported_and_left_out(width):
     rng = np.random.default_rng(14)
     for page in (10 ** 6, -1):
-        pool = Pool(rng, [300, 200], 2, 128)
+        pool = Pool(rng, [300, 200], 2, 128, width=width)
         pool.table[0, 2] = page
         pool.upload()
         q, qr = rounded(rng.standard_normal((2, 8, 128)), "bf16")
@@ -506,8 +516,11 @@ def test_attention_bad_data_is_reported_and_left_out():
         assert err == lr.LR_DEVERR_PAGE
         ref = orc.decode(qr, pool.kc, pool.vc, pool.ks, pool.vs, pool.table, pool.lens, 128 ** -0.5)
         check_attention((o, lse), ref, pool, qr, 128 ** -0.5, 300)
-    pool = Pool(rng, [256, 200], 2, 128)
-    pool.set_lens([1000, -4])
+    pool = Pool(rng, [256, 200], 2, 128, width=width)
+    pool.set_lens([1000, -4] if width is None else [64 * width + 1, -4])
+    if width is not None:  # clipped to the table's room, of which four pages are there
+        assert attend(pool, q)[2] == lr.LR_DEVERR_LEN | lr.LR_DEVERR_PAGE
+        return
     o, lse, err = attend(pool, q)
     assert err == lr.LR_DEVERR_LEN
     pool.lens[:] = [256, 0]
