@@ -657,13 +657,14 @@ cudaError_t launch_append(const Kv8AppendArgs& a, int sm_count, cudaStream_t st)
   const int units = a.n_tokens / kBlock + 2 * a.B;
   const int smem = ahead<T>() * 2 * 8 * (int)sizeof(T) * threads;
   // Heads are shared out among up to 8 CTAs, which fill the machine evenly to the end. Each finds the page's angles
-  // again, though, so with more pages than SMs a share has four query heads at least: 32K tokens of 32 + 8
-  // heads take 122 us with 8 shares, 127 with 4, 132 with one; of 8 + 8 heads 88, 73 and 68. Where most
-  // pages get a few tokens a share's beginning weighs more: 20 tokens each of 128 sequences 27 us
-  // with 8, 22 with 2.
+  // again, though, so with more pages than SMs a share has eight query heads at least. Of 32 + 8 heads, 8
+  // shares and 4: 32K tokens 122 and 127 us by themselves, 132 and 133 in a long run; 24 ragged sequences 76
+  // and 74; 200 tokens each of 128 sequences 112 and 108. Of 8 + 8 heads, 8, 2 and one: 88, 70 and 68.
+  // Where most pages get a few tokens a share's beginning weighs more: 20 tokens each of 128 sequences
+  // 27 us with 8, 24 with 4, 22 with 2.
   int ny = std::min(a.Hkv, 8);
   if (units > sm_count) {
-    ny = std::max(1, std::min(ny, a.Hq / 4));
+    ny = std::max(1, std::min(ny, a.Hq / 8));
     if (a.n_tokens < (long long)kBlock / 2 * a.B) ny = std::min(ny, 2);
   }
   void (*kernel)(Kv8AppendArgs, int) = kv8_append_kernel<T, Turn::kMixed>;
