@@ -384,9 +384,9 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
       mbar_wait_drain(&full[warp][j % R::kStages], (j / R::kStages) & 1, kWaitCycles / 4);
   if (bf16) empty_rows<__nv_bfloat16>(a, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
   else empty_rows<float>(a, blockIdx.x * kWarps + warp, gridDim.x * kWarps);
-  if (a.cluster && blockIdx.x == 0 && warp == kWarps - 1) {
-    const int bits = check_all(a);
-    if (lane == 0 && bits) atomicOr(&err, bits);
+  if (a.cluster && blockIdx.x == 0) {
+    const int bits = check_all(a, tid, NT);
+    if (bits) atomicOr(&err, bits);
   }
   __syncthreads();
   if (a.cluster) {

@@ -586,8 +586,8 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   } else if (warp == kLoads) {
     load_tiles(a, sh, &mk, &mv, wk);
     if (a.cluster) {
-      const int bits = blockIdx.x == 0 ? check_all(a) : 0;
-      if (lane == 0 && bits) atomicOr(sh.err(), bits);
+      const int bits = blockIdx.x == 0 ? check_all(a, lane, 32) : 0;
+      if (bits) atomicOr(sh.err(), bits);
     } else if (lane == 0) {
       write_pieces(a, wk);
     }

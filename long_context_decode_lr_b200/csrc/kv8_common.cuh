@@ -239,17 +239,21 @@ __device__ __forceinline__ Work small_work(const Kv8AttnArgs& a) {
   return wk;
 }
 
-// Small calls: the device checks of every length and attended page, by one warp of one CTA; the bits are in every lane.
-__device__ __forceinline__ int check_all(const Kv8AttnArgs& a) {
+// Small calls: the device checks of every length and attended page, by the threads [0, step) of one CTA. They go through the
+// whole table (2048 ids at most), an id with its sequence's length: loads that depend on one another, sequence by
+// sequence, made this CTA 49 us late with 256 sequences.
+__device__ __forceinline__ int check_all(const Kv8AttnArgs& a, int first, int step) {
   int bits = 0;
-  for (int b = 0; b < a.B; ++b) {
-    const int len = __ldg(a.lens + b);
+  const int ids = a.B * a.max_pages;
+#pragma unroll 8
+  for (int i = first; i < ids; i += step) {
+    const int b = (unsigned)i / (unsigned)a.max_pages, p = i - b * a.max_pages;
+    const int id = __ldg(a.table + i), len = __ldg(a.lens + b);
     if (len < 0 || len > a.max_pages * kBlock) bits |= LR_DEVERR_LEN;
     const Span sp = span_of(a, len);
-    for (int p = sp.page0 + (int)(threadIdx.x & 31); p * kBlock < sp.n; p += 32)
-      if ((unsigned)__ldg(a.table + (size_t)b * a.max_pages + p) >= (unsigned)a.n_pages) bits |= LR_DEVERR_PAGE;
+    if (p >= sp.page0 && p * kBlock < sp.n && (unsigned)id >= (unsigned)a.n_pages) bits |= LR_DEVERR_PAGE;
   }
-  return __reduce_or_sync(0xffffffffu, bits);
+  return bits;
 }
 
 // The CTA whose range holds unit t, for total units over `active` CTAs: largest c with

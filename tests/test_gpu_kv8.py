@@ -528,6 +528,35 @@ def test_attention_bad_data_is_reported_and_left_out(width):
     check_attention((o, lse), ref, pool, qr, 128 ** -0.5, 256)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("B", [100, 300])
+def test_attention_one_bad_page_of_a_large_batch(B, dtype):
+    """Reported and left out wherever it is attended, and only there."""
+    rng = np.random.default_rng(23)
+    lens = rng.integers(0, 257, B)
+    lens[[0, B // 2, B - 1]] = 256, 200, 130
+    pool = Pool(rng, lens, 1, 128, dtype, width=4)
+    q, qr = rounded(rng.standard_normal((B, 4, 128)), dtype)
+    table = pool.table.copy()
+    for b, page, window, expect in ((0, 3, 0, True), (B // 2, 0, 0, True), (B // 2, 3, 0, True), (B - 1, 2, 0, True),
+                                    (B - 1, 0, 130, True), (B - 1, 0, 67, True), (B - 1, 0, 66, False), (B - 1, 3, 0, False)):
+        pool.table[:] = table
+        pool.table[b, page] = pool.kc.shape[0]
+        pool.upload()
+        o, lse, err = attend(pool, q, window=window)
+        assert err == (lr.LR_DEVERR_PAGE if expect else 0), (b, page, window)
+        ref = orc.decode(qr, pool.kc, pool.vc, pool.ks, pool.vs, pool.table, pool.lens, 128 ** -0.5, window=window)
+        check_attention((o, lse), ref, pool, qr, 128 ** -0.5, 256)
+    pool.table[:] = table
+    pool.upload()
+    for b in (0, 37, B - 1):
+        lens = pool.lens.copy()
+        pool.set_lens(np.where(np.arange(B) == b, -1, lens))
+        assert attend(pool, q)[2] == lr.LR_DEVERR_LEN
+        pool.set_lens(lens)
+    assert attend(pool, q)[2] == 0
+
+
 def test_attention_shared_pages_strided_pool_other_stream():
     """Two sequences over the same pages give the same; K and V side by side in one pool; a side stream."""
     rng = np.random.default_rng(15)
