@@ -12,7 +12,9 @@
 // whole turns by itself and far positions lose nothing; sine and cosine take the top 32 bits.
 //
 // Measured (B200, 32 query and 8 KV heads of 128 bf16 numbers, all rotated): 32K tokens of one sequence
-// 122 us, 6.0 TB/s of the 738 MB read and written; one token for each of 64 sequences 3.4 us.
+// 127 us (133 in a long run), 5.8 TB/s of the 738 MB read and written; one token for each of 64 sequences 3.4 us.
+// fp32 335 us, 4.2 TB/s, rotated or not: its warps wait for the memory queue, with the issue slots and HBM half idle.
+// Lanes that exchange their 16-byte parts, so that an instruction covers whole sectors or lines, took 354 and 362.
 #include <algorithm>
 
 #include "kv8_common.cuh"
@@ -252,7 +254,7 @@ __global__ void __launch_bounds__(32 * kOneWarps) kv8_append_one_kernel(Kv8Appen
 // pairs up. The angles depend on row and chunk alone, so a thread finds its 8 sines and cosines once and
 // uses them for every head.
 //
-// Bound by memory (fp32, and rows with few query heads, by issue slots: a KV head costs a thread about 440
+// Bound by memory (rows with few query heads by issue slots: a KV head costs a thread about 440
 // instructions, the angles 500, a query head 90), if enough of it is asked for in time: a thread copies its own chunks to shared memory
 // with cp.async, kAhead heads ahead (query heads first, then a key and a value row per KV head), and reads
 // them back without a barrier. Keys and values meet at one barrier per KV head, for the largest magnitude.
