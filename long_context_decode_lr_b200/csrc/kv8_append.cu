@@ -18,6 +18,7 @@
 #include <algorithm>
 
 #include "kv8_common.cuh"
+#include "kv8_rules.h"
 
 namespace lr {
 namespace kv8 {
@@ -352,9 +353,9 @@ __device__ void check_ranges(const Kv8AppendArgs& a, int n_units, int* bits) {
       }
     }
     const NewTokens t = new_tokens(a, b);
-    const int page_i = u - unit_of(a, b), pg = t.p0 / kBlock + page_i;
-    if (page_i >= 0 && t.n && pg * kBlock < t.p0 + t.n &&
-        (unsigned)__ldg(a.table + (size_t)b * a.max_pages + pg) >= (unsigned)a.n_pages)
+    PageRows pr;
+    if (page_rows(t.p0, t.n, u - unit_of(a, b), pr) &&
+        (unsigned)__ldg(a.table + (size_t)b * a.max_pages + pr.page) >= (unsigned)a.n_pages)
       mine |= LR_DEVERR_PAGE;
   }
   if (mine) atomicOr(bits, mine);
@@ -427,13 +428,11 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
     b += n * step;
     len = min(step, len - n * step);
   }
-  const int page_i = u - unit_of(a, b);
   const NewTokens t = new_tokens(a, b);
-  if (page_i < 0 || !t.n) return;
-  const int pg = t.p0 / kBlock + page_i;                      // page of the sequence
-  const int first = max(t.p0, pg * kBlock), end = min(t.p0 + t.n, (pg + 1) * kBlock);
-  if (first >= end) return;
-  const int slot0 = first - pg * kBlock, rows = end - first;  // new rows slot0 .. slot0 + rows - 1
+  PageRows pr;
+  if (!page_rows(t.p0, t.n, u - unit_of(a, b), pr)) return;
+  const int pg = pr.page, first = pr.first;
+  const int slot0 = first - pg * kBlock, rows = pr.end - first;  // new rows slot0 .. slot0 + rows - 1
   const int token0 = t.start + (first - t.p0);
   int page = __ldg(a.table + (size_t)b * a.max_pages + pg);
   if ((unsigned)page >= (unsigned)a.n_pages) page = -1;

@@ -1,0 +1,41 @@
+"""The 8-bit paged cache at the edges of what its documentation allows, on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+from long_context_decode_lr_b200 import lowram as lr
+from oracle import kv8_oracle as orc
+
+from kv8_helpers import rounded
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from long_context_decode_lr_b200 import build
+    build.build()
+    lr.library()
+
+
+@pytest.mark.parametrize("n", [1, 64, 100])
+def test_append_fills_the_longest_table(n):
+    """The last tokens of a sequence of 64 (2^25 - 1) tokens: the page table has no entry behind them, and what lies
+    there (here: ids that no pool has) is not looked at."""
+    rng = np.random.default_rng(n)
+    width = (1 << 25) - 1
+    room = torch.full((width + 65,), -1, dtype=torch.int32, device="cuda")
+    pages = -(-n // 64)
+    room[width - pages:width] = torch.arange(pages, dtype=torch.int32, device="cuda")
+    kc, vc = (torch.zeros((pages, 1, 64, 64), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.full((pages, 1), 2.0 ** -24, device="cuda") for _ in range(2))
+    lens = torch.tensor([64 * width], dtype=torch.int32, device="cuda")
+    kv = lr.Kv8Pages(kc, vc, ks, vs, room[:width].view(1, width), lens, torch.bfloat16)
+    x, xr = rounded(rng.standard_normal((n, 1, 64)), "bf16")
+    cu, ws = torch.tensor([0, n], dtype=torch.int32, device="cuda"), lr.workspace(256)
+    lr.lr_kv8_append(kv, x, x, ws, cu_tokens=cu)
+    assert lr.lr_get_device_error(ws) == 0
+    want = [np.zeros((pages, 1, 64, 64), np.uint8) for _ in range(2)] + [np.full((pages, 1), 2.0 ** -24, np.float32) for _ in range(2)]
+    orc.append(*want, np.arange(pages)[None], [64 * pages], [0, n], xr, xr, [], 0, False)
+    for got, w in zip((kc, vc, ks, vs), want):
+        np.testing.assert_array_equal(got.cpu().numpy(), w)
