@@ -527,6 +527,8 @@ size_t lr_kv8_attn_workspace_bytes(const lr_kv8_pages* kv, int32_t n_q_heads);
  *          o_prev [B, Hq, hd] and lse_prev [B, Hq] fp32, both or neither.
  * Outputs: o [B, Hq, hd]; lse [B, Hq] fp32 or NULL. o may be o_prev, lse may be lse_prev.
  * A query head with a NaN or an infinite number gives NaN; a NaN code gives NaN where it is attended.
+ * Values of any magnitude that fp32 holds are summed without overflow, over any number of tokens (value
+ * scales under 2^-80 lose bits to it); scale * q . k_t must be finite in fp32.
  * Queries and weights enter the products as sums of narrower numbers: a bf16 query is exact down to 2^-15
  * of its head's largest number, an fp32 one to 2^-24; weights are right to 2^-24, with LR_BF16 and
  * head_dim 128 to 2^-12 (to 2^-28 of the largest weight of their 128 tokens where they are under 2^-16 of it).

@@ -339,7 +339,7 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
       ml[warp][1][hi] = l;
     }
     // dim d of a head is at d % (HD / 8) * 8 + d / (HD / 8): no two lanes meet in a bank
-    const float scale = unit * (1.f / 32768.f);
+    const float scale = unit * (1.f / 32768.f / kSumUnit);
 #pragma unroll
     for (int j = 0; j < HD / 8; ++j)
       *reinterpret_cast<float2*>(sums(warp, hi) + 8 * j + 2 * c) =

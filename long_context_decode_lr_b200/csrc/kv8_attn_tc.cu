@@ -48,7 +48,7 @@ constexpr int kColS = 0, kColO = 32;  // TMEM: two S of 16 columns, two O' of 2 
 // What the loading warp says of the tile in a stage.
 enum Flag { OK0 = 1, OK1 = 2, FIRST = 4, LAST = 8, WHOLE = 16, END = 32 };
 struct __align__(16) Meta {
-  float ks[2], vs[2];    // scales of its two pages
+  float ks[2], vs[2];    // scales of its two pages, of values for sums in units of kSumUnit with weights times 256
   int t0, lo, n, flags;  // its first token, the attended ones; which pages there are (OK0, OK1), first or last
                          // tile of the segment here, all of the segment here, no tile: the end
   int head, slot;        // b * Hkv + h, and where a piece of it goes
@@ -212,8 +212,8 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
         Meta m;
         m.ks[0] = t.ks;
         m.ks[1] = ks1;
-        m.vs[0] = t.vs;
-        m.vs[1] = vs1;
+        m.vs[0] = t.vs * (1.f / 256.f / kSumUnit);
+        m.vs[1] = vs1 * (1.f / 256.f / kSumUnit);
         m.t0 = (t.at.sp.page0 + t.at.tile * kTilePages) * kBlock;
         m.lo = t.at.sp.lo;
         m.n = t.at.sp.n;
@@ -384,7 +384,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
       for (int y = 0; y < 2; ++y)
         o[y] = fmaf(__uint_as_float(d[y][8 + g]), 1.f / 1024.f,
                     fmaf(__uint_as_float(d[y][4 + g]), 1.f / 32.f, __uint_as_float(d[y][g])));
-      acc[g] = fmaf(acc[g], old[g], fmaf(o[0], vs0, o[1] * vs1) * (now[g] * (1.f / 256.f)));
+      acc[g] = fmaf(acc[g], old[g], fmaf(o[0], vs0, o[1] * vs1) * now[g]);
     }
   };
   for (uint32_t it = 0;; ++it) {

@@ -313,10 +313,14 @@ struct Walk : Place {
   __device__ bool whole() const { return tile0 == 0 && tile1 == sp.tiles; }
 };
 
+// Sums of weights times values are kept in units of 2^32: a weight is 1 at most, so no number of tokens that an int
+// holds takes them out of fp32's range, whatever finite values the codes and scales stand for.
+constexpr float kSumUnit = 4294967296.f;
+
 // Output of one (sequence, query head): acc / l with the scores' reference m (2^x units), joined with
 // the earlier partial result where there is one.
 struct Joined {
-  float inv, w_prev;  // o = acc * inv + o_prev * w_prev
+  float inv, w_prev;  // o = acc * inv + o_prev * w_prev, acc in units of kSumUnit
   float top, sum;     // lse = ln 2 (top + log2 sum)
   __device__ __forceinline__ float lse() const {
     return sum == 0.f ? -CUDART_INF_F : 0.6931471805599453f * (top + log2f(sum));
@@ -336,7 +340,7 @@ __device__ __forceinline__ Joined join_with(float m, float l, float prev) {
   const float wp = lp == -CUDART_INF_F ? 0.f : exp2f(lp - j.top);
   j.sum = fmaf(l, w, wp);
   const float r = __frcp_rn(j.sum);
-  j.inv = w * r;
+  j.inv = w * r * kSumUnit;
   j.w_prev = wp * r;  // NaN where the sum is, with or without an earlier part
   return j;
 }

@@ -49,7 +49,7 @@ struct Kv8AttnArgs {
   int* err;
   int* cta_err;           // [n_cta] device error bits of each CTA, joined into *err
   void* split;            // [n_cta] kv8::Pieces: the split segment that each CTA wrote down
-  float* part;            // [2 n_cta] slots of part_stride floats: acc [G, hd], max [8], sum [8]
+  float* part;            // [2 n_cta] slots of part_stride floats: acc [G, hd] (in units of kv8::kSumUnit), max [8], sum [8]
   int n_cta;
   int part_stride;
   int cluster;            // 0, or CTAs of a cluster that has a segment to itself and joins it (small calls)

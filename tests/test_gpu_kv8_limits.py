@@ -6,7 +6,7 @@ import torch
 from long_context_decode_lr_b200 import lowram as lr
 from oracle import kv8_oracle as orc
 
-from kv8_helpers import rounded
+from kv8_helpers import Pool, attend, check_attention, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +39,29 @@ def test_append_fills_the_longest_table(n):
     orc.append(*want, np.arange(pages)[None], [64 * pages], [0, n], xr, xr, [], 0, False)
     for got, w in zip((kc, vc, ks, vs), want):
         np.testing.assert_array_equal(got.cpu().numpy(), w)
+
+
+@pytest.mark.parametrize("width", [None, 600], ids=["", "room_for_more"])
+@pytest.mark.parametrize("hd,dtype", [(128, "bf16"), (64, "f32"), (256, "bf16")])
+def test_attention_over_the_largest_values(hd, dtype, width):
+    """Values up to 3e38, as lr_kv8_append stores them: their sum over the tokens is far out of fp32's range, their
+    weighted mean is not. Pages of small values between them, an earlier part as large."""
+    rng = np.random.default_rng(hd)
+    pool = Pool(rng, [500, 64, 3], 2, hd, dtype, width=width, mixed=False)
+    for b, n in enumerate(pool.lens):
+        for i in range(-(-int(n) // 64)):
+            if i % 3 == 1:
+                continue
+            page, rows = pool.table[b, i], min(64, int(n) - 64 * i)
+            pool.vs[page] = 2.0 ** 120
+            pool.vc[page, :, :rows] = orc.e4m3_codes(rng.uniform(200, 225, (2, rows, hd)))  # 2.7e38 to 3e38
+    pool.upload()
+    q, qr = rounded(0.1 * rng.standard_normal((3, 8, hd)), dtype)  # near equal weights
+    po, por = rounded(rng.uniform(2e38, 3e38, (3, 8, hd)), dtype)
+    pl = rng.uniform(3, 7, (3, 8)).astype(np.float32)
+    for prev, ref_prev in ((None, ()), ((po, torch.from_numpy(pl).cuda()), (por, pl.astype(np.float64)))):
+        o, lse, err = attend(pool, q, prev=prev)
+        assert err == 0
+        ref = orc.decode(qr, pool.kc, pool.vc, pool.ks, pool.vs, pool.table, pool.lens, hd ** -0.5, 0, *ref_prev)
+        assert np.abs(ref[0]).max() > 1.5e38
+        check_attention((o, lse), ref, pool, qr, hd ** -0.5, 500)
