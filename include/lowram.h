@@ -481,8 +481,8 @@ size_t lr_kv8_append_workspace_bytes(const lr_kv8_pages* kv);
  *   scale = max(scale, fresh) where the page already holds tokens of the sequence: if that is
  *           larger than the old scale, their codes become round(code * old / scale);
  *   scale = fresh where it does not (what the page and its scale held before is not read);
- *   code  = round(x / scale), to nearest even; NaN and infinities become NaN codes and do not
- *           count towards a.
+ *   code  = round(x / scale), to nearest even, x / scale one fp32 division (exact where the scale is a
+ *           power of two); NaN and infinities become NaN codes and do not count towards a.
  * Keys are rotated in fp32 and rounded once, to the code. Rows behind the new tokens and every
  * other page keep their bytes. The result does not depend on the order of execution; calls with
  * the same new tokens in the same places may be repeated.

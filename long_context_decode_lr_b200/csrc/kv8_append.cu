@@ -61,6 +61,9 @@ __device__ __forceinline__ float or_nan(float x) { return fabsf(x) <= 3.40282346
 __device__ __forceinline__ uint32_t codes2(float lo, float hi, float inv) {
   return e4m3x2(or_nan(lo) * inv, or_nan(hi) * inv);
 }
+// A page may hold a scale of the caller's that is no power of two, and then its fp32 reciprocal is a rounded one:
+// numbers are divided. (Where no page does, that costs a call of one token under 0.1 us and a mixed one 2 of 71 us.)
+__device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
 
 // Four codes scaled again by `ratio`.
 __device__ __forceinline__ uint32_t rescale4(uint32_t u, float ratio) {
@@ -157,7 +160,7 @@ __device__ __forceinline__ void append_one(const Kv8AppendArgs& a, uint8_t* code
 #pragma unroll
     for (int e = 0; e < 4; ++e) top = max(top, finite_bits(x[u][e]));
   const float fresh = pow2(scale_exp(__reduce_max_sync(0xffffffffu, top)));
-  const float s = fmaxf(held, fresh), inv = 1.f / s;
+  const float s = fmaxf(held, fresh);
   if (slot > 0 && s > held) {
     const float ratio = held / s;
     for (int i = lane; i < slot * a.hd / 4; i += 32) {
@@ -168,14 +171,20 @@ __device__ __forceinline__ void append_one(const Kv8AppendArgs& a, uint8_t* code
   __syncwarp();
   if (lane == 0 && s != held) *at = s;
   uint8_t* row = head + (size_t)slot * a.hd;
+  const float inv = __frcp_rn(s);
 #pragma unroll
   for (int u = 0; u < Q; ++u) {
     const int i = lane + 32 * u;
     if (i >= quads) continue;
     int c0, c1;
     quad_dims(a, i, c0, c1);
-    *reinterpret_cast<uint16_t*>(row + c0) = (uint16_t)codes2(x[u][0], x[u][1], inv);
-    *reinterpret_cast<uint16_t*>(row + c1) = (uint16_t)codes2(x[u][2], x[u][3], inv);
+    if (is_pow2(s)) {
+      *reinterpret_cast<uint16_t*>(row + c0) = (uint16_t)codes2(x[u][0], x[u][1], inv);
+      *reinterpret_cast<uint16_t*>(row + c1) = (uint16_t)codes2(x[u][2], x[u][3], inv);
+    } else {
+      *reinterpret_cast<uint16_t*>(row + c0) = (uint16_t)codes2(__fdiv_rn(x[u][0], s), __fdiv_rn(x[u][1], s), 1.f);
+      *reinterpret_cast<uint16_t*>(row + c1) = (uint16_t)codes2(__fdiv_rn(x[u][2], s), __fdiv_rn(x[u][3], s), 1.f);
+    }
   }
 }
 
@@ -308,6 +317,13 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {  // nu
   u.x = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
   u.y = e4m3x2(x[4], x[5]) | (e4m3x2(x[6], x[7]) << 16);
   return u;
+}
+
+__device__ __forceinline__ uint2 divided_codes8(const float (&v)[8], float s) {
+  float x[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(v[i], s);
+  return codes8(x, 1.f);
 }
 
 // Sines, negative sines and cosines of a thread's 8 angles.
@@ -627,8 +643,8 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
             kx[x][i] = or_nan(kx[x][i]);
           }
         }
-        *reinterpret_cast<uint2*>(head[0] + row + at) = codes8(kx[x], ik);
-        *reinterpret_cast<uint2*>(head[1] + row + at) = codes8(v, iv);
+        *reinterpret_cast<uint2*>(head[0] + row + at) = is_pow2(now[0]) ? codes8(kx[x], ik) : divided_codes8(kx[x], now[0]);
+        *reinterpret_cast<uint2*>(head[1] + row + at) = is_pow2(now[1]) ? codes8(v, iv) : divided_codes8(v, now[1]);
       }
     }
     if (in) {

@@ -65,3 +65,38 @@ def test_attention_over_the_largest_values(hd, dtype, width):
         ref = orc.decode(qr, pool.kc, pool.vc, pool.ks, pool.vs, pool.table, pool.lens, hd ** -0.5, 0, *ref_prev)
         assert np.abs(ref[0]).max() > 1.5e38
         check_attention((o, lse), ref, pool, qr, hd ** -0.5, 500)
+
+
+@pytest.mark.parametrize("rot,inter", [(0, False), (128, False), (128, True), (64, False)])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("single", [False, True])
+def test_append_to_a_page_whose_scale_is_no_power_of_two(single, dtype, rot, inter):
+    """A page written by somebody else, with scales 3 and 0.7: codes are those of the fp32 quotient, numbers halfway
+    between two codes and their neighbours among them. Rotated keys are not compared, their values are."""
+    rng = np.random.default_rng(rot + inter)
+    mids = (orc.E4M3[:0x7E] + orc.E4M3[1:0x7F]) / 2
+    mids = np.resize(mids[mids < 200], 128).astype(np.float32)
+    for s in (np.float32(3.0), np.float32(0.7)):
+        pool = Pool(rng, [5], 2, 128, dtype, room=[64])
+        for scale in (pool.ks, pool.vs):
+            scale[pool.table[0, 0]] = s
+        pool.upload()
+        pool.set_lens([6])
+        x = np.stack([mids * s, np.nextafter(-mids * s, np.float32(1e9))])[None]  # [1, 2 heads, 128]
+        xd, xr = rounded(x, dtype)
+        quotient = (xr.astype(np.float32) / s).astype(np.float64)
+        cu = None if single else torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+        rope = None
+        if rot:
+            inv = torch.from_numpy((1 / 10000.0 ** (np.arange(0, rot, 2) / rot)).astype(np.float32)).cuda()
+            rope = lr.Rope(inv, rot, inter)
+        ws = lr.workspace(256)
+        lr.lr_kv8_append(pool.kv, xd, xd, ws, cu_tokens=cu, rope=rope)
+        assert lr.lr_get_device_error(ws) == 0
+        kc, vc, ks, vs = pool.arrays()
+        page = pool.table[0, 0]
+        assert (vs[page] == s).all() and (ks[page] >= s).all()
+        np.testing.assert_array_equal(vc[page, :, 5], orc.e4m3_codes(quotient)[0])
+        np.testing.assert_array_equal(vc[page, :, :5], pool.vc[page, :, :5])
+        if not rot:
+            np.testing.assert_array_equal(kc[page, :, 5], orc.e4m3_codes(quotient)[0])
