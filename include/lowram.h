@@ -406,7 +406,7 @@ lr_status lr_decode_attn_noalloc(const lr_cache_shape* shape, int32_t layer, int
 
 /*
  * lr_decode_attn_lse -- lr_decode_attn that also returns the log-sum-exp of every query head,
- *   lse[b, hq] = log sum_{t in S} exp(scale * q[b, hq] . k~_t)   (-inf for an empty S),
+ *   lse[b, hq] = log sum_{t in S} exp(scale * q[b, hq] . k~_t)   (-inf for an empty S, NaN where a score is),
  * which lr_decode_attn_kv8 takes to join more tokens to the same softmax.
  * Output: lse [B, Hq] fp32. Everything else is as lr_decode_attn.
  */

@@ -281,9 +281,9 @@ __global__ void __launch_bounds__(CT) decode_combine_kernel(DecodeArgs a) {
     if (lane == 0) {
       s_lc = lc;
       s_lt = lt;
-      // m is the largest score of all: the sum is at least 1, or the set is empty
-      if (a.lse && jc == 0)
-        a.lse[(size_t)b * Hq + qh] = m == -CUDART_INF_F ? -CUDART_INF_F : m + logf(lc + lt);
+      // m is the largest score of all: the sum is at least 1, or the set is empty, or a score is NaN (which no maximum
+      // shows, but the sum does)
+      if (a.lse && jc == 0) a.lse[(size_t)b * Hq + qh] = lc + lt == 0.f ? -CUDART_INF_F : m + logf(lc + lt);
     }
   }
   __syncthreads();

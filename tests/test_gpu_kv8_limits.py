@@ -6,6 +6,7 @@ import torch
 from long_context_decode_lr_b200 import lowram as lr
 from oracle import kv8_oracle as orc
 
+import helpers as H
 from kv8_helpers import Pool, attend, check_attention, rounded
 
 pytestmark = pytest.mark.gpu
@@ -100,3 +101,28 @@ def test_append_to_a_page_whose_scale_is_no_power_of_two(single, dtype, rot, int
         np.testing.assert_array_equal(vc[page, :, :5], pool.vc[page, :, :5])
         if not rot:
             np.testing.assert_array_equal(kc[page, :, 5], orc.e4m3_codes(quotient)[0])
+
+
+@pytest.mark.parametrize("path", ["pair", "general"])
+def test_nan_query_over_the_packed_context_is_not_an_empty_context(path, monkeypatch):
+    """The log-sum-exp of a head whose scores are NaN is NaN, so that the joined result is too: -inf would leave the
+    packed context out without a word."""
+    monkeypatch.setenv("LOWRAM_DECODE_PATH", path)
+    p = H.packed_problem(H.small(T=300))
+    w = p.w
+    q, _ = H.queries(p, 0)
+    q = q.clone()
+    q[0, 1, 3] = float("nan")
+    shape = H.shape_of(w)
+    o, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ws = lr.workspace(lr.lr_decode_workspace_bytes(shape, w.n_q_heads, 0))
+    lr.lr_decode_attn_lse(shape, 0, w.n_q_heads, q, p.st["A"], p.st["Bt"], H.gpu_predictor(p), p.st["idx"], p.st["val"],
+                          p.st["ptr"], p.k, None, 0, 0.0, o, lse, ws)
+    want = torch.zeros(w.n_q_heads, dtype=torch.bool, device="cuda")
+    want[1] = True
+    assert torch.equal(torch.isnan(lse[0]), want) and torch.isfinite(lse[0][~want]).all()
+    pool = Pool(np.random.default_rng(0), [70], w.n_kv_heads, w.head_dim)
+    clean, _ = H.queries(p, 0)
+    joined, lse2, _ = attend(pool, clean, prev=(o, lse))
+    assert torch.isnan(joined[0, 1]).all() and torch.equal(torch.isnan(lse2[0]), want)
+    assert torch.isfinite(joined[0][~want]).all()
