@@ -459,8 +459,9 @@ typedef struct lr_kv8_pages {
  * pair j of a token at position pos turns by the angle pos * inv_freq[j],
  *     (x0, x1) -> (x0 cos - x1 sin, x1 cos + x0 sin),
  * where pair j is dims (j, rot_dim / 2 + j), or (2j, 2j + 1) with interleaved = 1.
- * inv_freq [rot_dim / 2] fp32 in radians per token. The angle is reduced exactly: sine and cosine are
- * right to about 5e-7 at every position an int32 can hold (to fp32 rounding where dtype is LR_F32).
+ * inv_freq [rot_dim / 2] fp32 in radians per token, of magnitude up to 2^32. Angles are reduced in 64-bit
+ * fractions of a turn: at every position an int32 can hold, sine and cosine are right to 2^-22 where dtype is
+ * LR_F32 and to 2^-20 where it is LR_BF16.
  */
 typedef struct lr_rope {
   const float* inv_freq;

@@ -9,7 +9,7 @@
 // between the maximum and the rounding.
 //
 // Angles: a pair's frequency becomes a 64-bit fraction of a turn, so position * fraction wraps at
-// whole turns by itself and far positions lose nothing; sine and cosine take the top 32 bits.
+// whole turns by itself and stays right to 2^-32 of a turn at far positions; sine and cosine take the top 32 bits.
 //
 // Measured (B200, 32 query and 8 KV heads of 128 bf16 numbers, all rotated): 32K tokens of one sequence
 // 127 us (133 in a long run), 5.8 TB/s of the 738 MB read and written; one token for each of 64 sequences 3.4 us.
@@ -26,13 +26,17 @@ namespace {
 
 constexpr int kMinExp = -24;  // smallest scale 2^-24: numbers under 2^-34 become 0
 
+// `radians` / 2 pi modulo 1, in 2^-64: off by one or two units, which at position 2^31 is 2^-32 of a turn (with 1 / 2 pi
+// in one fp64 number it was 2^-22 of inv_freq there). 1 / 2 pi is the sum of two fp64 numbers and the product with the first
+// is taken exactly, as a rounded product and what the rounding left.
 __device__ __forceinline__ uint64_t turn_fraction(float radians) {
-  double t = (double)radians * 0.15915494309189533577;  // / 2 pi
-  t -= floor(t);
-  return (uint64_t)(t * 18446744073709551616.0);
+  constexpr double kHi = 0.15915494309189535, kLo = -9.839338337591243e-18, k64 = 18446744073709551616.0;
+  const double f = radians, t = __dmul_rn(f, kHi), rest = __fma_rn(f, kLo, __fma_rn(f, kHi, -t));
+  return (uint64_t)__double2ll_rn((t - rint(t)) * k64) + (uint64_t)__double2ll_rn(rest * k64);
 }
-// T: what the rotated numbers are rounded to. bf16 takes the hardware's sine and cosine (within 2^-21 on one
-// turn, against half a step of 2^-9; with sincospif the angles were a fifth of all instructions).
+// Within 2^-22 for fp32: the angle, a number of half turns up to 1, is rounded to 24 bits (pi 2^-25), and sincospif to
+// its last place. bf16 takes the hardware's sine and cosine, within 2^-20: 2^-21.2 on one turn, and the radians
+// are rounded twice (half a step of bf16 is 2^-9; with sincospif the angles were a fifth of all instructions).
 template <typename T>
 __device__ __forceinline__ void sin_cos(uint64_t fraction, int pos, float& s, float& c) {
   const int32_t turns = (int32_t)((fraction * (uint64_t)(uint32_t)pos) >> 32);

@@ -1,4 +1,6 @@
 """The 8-bit paged cache at the edges of what its documentation allows, on the GPU."""
+from fractions import Fraction
+
 import numpy as np
 import pytest
 import torch
@@ -7,7 +9,7 @@ from long_context_decode_lr_b200 import lowram as lr
 from oracle import kv8_oracle as orc
 
 import helpers as H
-from kv8_helpers import Pool, attend, check_attention, rounded
+from kv8_helpers import DT, HALF, Pool, attend, check_attention, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -126,3 +128,31 @@ def test_nan_query_over_the_packed_context_is_not_an_empty_context(path, monkeyp
     joined, lse2, _ = attend(pool, clean, prev=(o, lse))
     assert torch.isnan(joined[0, 1]).all() and torch.equal(torch.isnan(lse2[0]), want)
     assert torch.isfinite(joined[0][~want]).all()
+
+
+TWO_PI = 2 * Fraction(314159265358979323846264338327950288419716939937510582097494459230781640628620899, 10 ** 80)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("pos", [0, 1, 12345, 2 ** 30 + 7, 64 * ((1 << 25) - 1) - 1])
+@pytest.mark.parametrize("single", [False, True])
+def test_rotation_angles_at_every_position(single, pos, dtype):
+    """Queries (1, 0) turn into cosine and sine: within 2^-22 (fp32) or 2^-20 (bf16) of the exact angle's, plus the
+    output's rounding, for frequencies under and over one radian per token, positive and negative."""
+    inv = np.array([0.0, 1.0, 3.0, 6.2, -0.7, 100.5, 1e-6, 3e9] + list(np.random.default_rng(1).uniform(-6.3, 6.3, 56)), np.float32)
+    width = pos // 64 + 1
+    table = torch.zeros((1, width), dtype=torch.int32, device="cuda")
+    kc, vc = (torch.zeros((1, 1, 64, 128), dtype=torch.uint8, device="cuda") for _ in range(2))
+    ks, vs = (torch.ones((1, 1), device="cuda") for _ in range(2))
+    kv = lr.Kv8Pages(kc, vc, ks, vs, table, torch.tensor([pos + 1], dtype=torch.int32, device="cuda"), DT[dtype])
+    x = torch.zeros((1, 1, 128), dtype=DT[dtype], device="cuda")
+    x[:, :, :64] = 1.0
+    out, ws = torch.empty_like(x), lr.workspace(256)
+    cu = None if single else torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    lr.lr_kv8_append(kv, x, x, ws, cu_tokens=cu, rope=lr.Rope(torch.from_numpy(inv).cuda(), 128), q=x, q_out=out)
+    assert lr.lr_get_device_error(ws) == 0
+    got = out[0, 0].double().cpu().numpy()
+    angles = [Fraction(float(f)) * pos for f in inv]
+    angles = np.array([float(a - TWO_PI * (a // TWO_PI)) for a in angles])
+    want = np.concatenate([np.cos(angles), np.sin(angles)])
+    assert (np.abs(got - want) <= (2.0 ** -20 if dtype == "bf16" else 2.0 ** -22) + HALF[dtype] * np.abs(want)).all()
