@@ -530,9 +530,11 @@ size_t lr_kv8_attn_workspace_bytes(const lr_kv8_pages* kv, int32_t n_q_heads);
  * A query head with a NaN or an infinite number gives NaN; a NaN code gives NaN where it is attended.
  * Values of any magnitude that fp32 holds are summed without overflow, over any number of tokens (value
  * scales under 2^-80 lose bits to it); scale * q . k_t must be finite in fp32.
- * Queries and weights enter the products as sums of narrower numbers: a bf16 query is exact down to 2^-15
- * of its head's largest number, an fp32 one to 2^-24; weights are right to 2^-24, with LR_BF16 and
- * head_dim 128 to 2^-12 (to 2^-28 of the largest weight of their 128 tokens where they are under 2^-16 of it).
+ * Scores, sums and exponentials (right to 2^-22) are fp32; queries and weights enter the products as sums of
+ * narrower numbers. LR_BF16 with head_dim 128: a query number is exact down to 2^-14 of its head's largest and right to
+ * 2^-22 of that below, a weight is right to 2^-11, or to 2^-27 of the largest of its 128 tokens where it is under 2^-17
+ * of that. Other shapes: both are right to 2^-23, or to 2^-50 of the head's largest query number or weight where they
+ * are small; tokens of a page whose value scale is under 2^-64 of the largest before it, to 2^-106 of that one each.
  * Device checks: a length out of bounds is clipped to [0, 64 max_pages] (LR_DEVERR_LEN), a page id
  * out of range leaves that page's tokens out (LR_DEVERR_PAGE).
  */

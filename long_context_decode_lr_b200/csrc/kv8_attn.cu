@@ -4,7 +4,8 @@
 // Products by mma.sync (m16n8k16, fp16 in, fp32 sums): codes are exact in fp16, one conversion for two of them,
 // and what multiplies them is a sum of two fp16 numbers, the second one 2^11 times as fine:
 //   q = 2^e (q0 + q1 / 2048),   p = (p0 + p1 / 2048) / 2^15,
-// each right to 2^-24, as good as fp32. The 16 rows of an operand are 8 query heads times two terms: row h
+// each right to 2^-23 (the second term rounds what the first leaves over, up to 2^-11 of it, to 11 bits), or to 2^-50 of
+// the largest where it is an fp16 subnormal. The 16 rows of an operand are 8 query heads times two terms: row h
 // and row h + 8, which the same lanes hold, so
 //   S = Q K^T   (16 x 8 tokens): lane 4h + c has both terms of head h for tokens 2c and 2c + 1, and so
 //   O = P V     (16 x 8 dims) takes the weights from the registers that the scores were in.

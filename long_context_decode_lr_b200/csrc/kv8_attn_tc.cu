@@ -5,10 +5,10 @@
 // a wider type would cost more issue slots than the bytes cost time. What multiplies them is
 // therefore written as a sum of e4m3 numbers too, each term taking four more bits of what the ones
 // before leave over:
-//   q = 2^e (q1 + q2 / 32)              exact for a bf16 number down to 2^-15 of the head's largest
+//   q = 2^e (q1 + q2 / 32)              exact for a bf16 number down to 2^-14 of the head's largest
 //                                       (below that off by 2^-22 of it at most);
-//   p = (p1 + p2 / 32 + p3 / 1024) / 256, p rounded to fp16 first: 2^-12 relative at most, 2^-28 absolute
-//                                       for p under 2^-16, p relative to the largest of the tile.
+//   p = (p1 + p2 / 32 + p3 / 1024) / 256, p rounded to fp16 first: 2^-11 relative at most, and 2^-27 absolute
+//                                       for p under 2^-17, p relative to the largest of the tile.
 // Every term is a column of its own, so a tile's products are
 //   S  [128 tokens x 16]     = K q1 | K q2             (M 128, N 16, K 128)
 //   O' [128 dims x 3 heads]  = V^T p1 | V^T p2 | V^T p3 (M 128, N 16 or 32, K 64) for each of the two pages,
