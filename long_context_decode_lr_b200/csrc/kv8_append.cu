@@ -274,9 +274,6 @@ __global__ void __launch_bounds__(32 * kOneWarps) kv8_append_one_kernel(Kv8Appen
 // them back without a barrier. Keys and values meet at one barrier per KV head, for the largest magnitude.
 // That maximum is taken without a look at what is infinite (NaN drops out by itself); only a page where it
 // comes out infinite is gone through again.
-//
-// Sequence b's pages are the units from cu[b] / 64 + 2 b on: always enough of them (n tokens touch
-// at most n / 64 + 2 pages), without a scan over the batch.
 
 template <typename T>
 struct Row8;  // 8 consecutive numbers
@@ -351,8 +348,6 @@ __device__ __forceinline__ void rotate_within(float (&x)[8], const Angles& t) {
   for (int i = 0; i < 2; ++i) turn(t, AT / 2 + i, x[4 * i], x[4 * i + 2], x[4 * i + 1], x[4 * i + 3]);
 }
 
-__device__ __forceinline__ int unit_of(const Kv8AppendArgs& a, int b) { return __ldg(a.cu + b) / kBlock + 2 * b; }
-
 // The device checks of every sequence and page, by one CTA: the word is written, so nothing has to clear it
 // before.
 __device__ void check_ranges(const Kv8AppendArgs& a, int n_units, int* bits) {
@@ -362,16 +357,7 @@ __device__ void check_ranges(const Kv8AppendArgs& a, int n_units, int* bits) {
   for (int b = threadIdx.x; b < a.B; b += blockDim.x)
     if (!new_tokens(a, b).ok) mine |= LR_DEVERR_LEN;
   for (int u = threadIdx.x; u < n_units; u += blockDim.x) {
-    int b = 0, len = a.B;  // largest b with unit_of(b) <= u
-    while (len > 1) {
-      const int half = len / 2;
-      if (unit_of(a, b + half) <= u) {
-        b += half;
-        len -= half;
-      } else {
-        len = half;
-      }
-    }
+    const int b = sequence_of_unit(a, u);
     const NewTokens t = new_tokens(a, b);
     PageRows pr;
     if (page_rows(t.p0, t.n, u - unit_of(a, b), pr) &&
@@ -439,7 +425,7 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
     if (blockIdx.y == 0) check_ranges(a, n_units, (int*)top);
     return;
   }
-  // the sequence of this unit: largest b with unit_of(b) <= u, 32 candidates a round
+  // the sequence of this unit, as sequence_of_unit finds it, 32 candidates a round
   int b = 0, len = a.B;
   while (len > 1) {
     const int step = (len + 31) / 32, at = b + lane * step;
@@ -675,7 +661,7 @@ cudaError_t launch_append(const Kv8AppendArgs& a, int sm_count, cudaStream_t st)
     return cudaGetLastError();
   }
   const int threads = kBlock * ((a.hd + 15) / 16);
-  const int units = a.n_tokens / kBlock + 2 * a.B;
+  const int units = n_units(a);
   const int smem = ahead<T>() * 2 * 8 * (int)sizeof(T) * threads;
   // Heads are shared out among up to 8 CTAs, which fill the machine evenly to the end. Each finds the page's angles
   // again, though, so with more pages than SMs a share has eight query heads at least. Of 32 + 8 heads, 8

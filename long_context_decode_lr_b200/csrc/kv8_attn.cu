@@ -111,9 +111,9 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
   __syncthreads();
   prefetch_inputs(a);
   grid_dependency();
-  Walk k(a, a.cluster ? small_work(a) : find_work<NT>(a, scratch));
+  Walk<Kv8AttnArgs> k(a, a.cluster ? small_work(a, blockIdx.x) : find_work<NT>(a, scratch));
   if (blockIdx.x == 0 && k.wk.bad_len) atomicOr(&err, LR_DEVERR_LEN);
-  if (tid == 0 && !a.cluster) write_pieces(a, k.wk);
+  if (tid == 0 && !a.cluster) reinterpret_cast<Pieces*>(a.split)[blockIdx.x] = pieces_of(a, k.wk, blockIdx.x);
   uint32_t stages = 0;  // copied to so far, by this warp
   bool ok = true;       // once a wait has failed the rest runs through without waiting: nobody is left at a barrier
   while (k.next()) {
@@ -347,7 +347,7 @@ __global__ void __launch_bounds__(NT, resident(HD)) kv8_attn_kernel(Kv8AttnArgs 
           make_float2(fmaf(acc[j][2], 1.f / 2048.f, acc[j][0]) * scale, fmaf(acc[j][3], 1.f / 2048.f, acc[j][1]) * scale);
     __syncthreads();
     const bool whole = k.whole();
-    float* slot = whole ? nullptr : a.part + (size_t)piece_slot(k.wk, k.seg_first) * a.part_stride;
+    float* slot = whole ? nullptr : a.part + (size_t)piece_slot(k.wk, blockIdx.x, k.seg_first) * a.part_stride;
     for (int g = warp; g < G; g += kWarps) {
       float top = -CUDART_INF_F;
 #pragma unroll
@@ -417,7 +417,6 @@ cudaError_t launch_attn_any(const Kv8AttnArgs& a, bool bf16, cudaStream_t st) {
 
 constexpr int JT = 128;
 constexpr int kMaxCtas = 1024;
-constexpr int kSmallCtas = 256;  // of a small call: clusters of 8 find room for all of them at once
 
 template <typename T>
 __global__ void __launch_bounds__(JT, 8) kv8_join_kernel(Kv8AttnArgs a) {
@@ -538,18 +537,8 @@ Kv8AttnPlan plan_kv8_attn(const lr_kv8_pages& kv, int n_q_heads, int sm_count) {
   const long long most = (long long)kv.batch * kv.n_kv_heads * ((kv.max_pages + 1) / 2 + kv8::kSegmentUnits);  // units
   p.tensor = kv.dtype == LR_BF16 && kv.head_dim == 128;
   p.n_cta = (int)std::max(1LL, std::min<long long>(most, std::min((p.tensor ? 2 : kv8::resident(kv.head_dim)) * sm_count, kv8::kMaxCtas)));
-  // Small calls in one launch: a cluster for every segment, which joins it itself, if that gives no CTA more than
-  // four tiles (two with mma.sync). 8 KV heads, bf16: 1000 tokens 7.4 us and 7.9 from Python, with the second
-  // kernel 9.0 and 9.7; 4000 tokens 9.8 and 9.9. fp32: 2000 tokens 10.3 and 10.2, 4000 tokens 13.4 and 11.4.
-  const long long segments = (long long)kv.batch * kv.n_kv_heads, tiles = (kv.max_pages + 1) / 2;
-  if (segments > 0 && segments <= kv8::kSmallCtas) {
-    int c = 8;
-    while (c > 1 && (segments * c > kv8::kSmallCtas || c / 2 >= tiles)) c /= 2;
-    if (tiles <= (p.tensor ? 4 : 2) * c) {
-      p.cluster = c;
-      p.n_cta = (int)segments * c;
-    }
-  }
+  p.cluster = kv8::small_cluster(kv.batch, kv.n_kv_heads, kv.max_pages, p.tensor);
+  if (p.cluster) p.n_cta = kv.batch * kv.n_kv_heads * p.cluster;
   p.part_stride = G * kv.head_dim + 16;
   p.split_off = 256;
   p.cta_err_off = p.split_off + (size_t)p.n_cta * sizeof(kv8::Pieces);

@@ -220,7 +220,7 @@ __device__ void load_tiles(const Kv8AttnArgs& a, const Shared& sh, const CUtenso
         m.flags = (t.id >= 0 ? OK0 : 0) | (id1 >= 0 ? OK1 : 0) | (first ? FIRST : 0) | (last ? LAST : 0) |
                   (t.at.seg_first >= wk.begin && t.at.seg_first + t.at.sp.tiles <= wk.end ? WHOLE : 0);
         m.head = head;
-        m.slot = piece_slot(wk, t.at.seg_first);
+        m.slot = piece_slot(wk, blockIdx.x, t.at.seg_first);
         *sh.meta(s) = m;
         mbar_arrive(sh.bar(K_FULL + s));
       }
@@ -579,7 +579,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
   const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(tmem_holder);
   prefetch_inputs(a);
   grid_dependency();
-  const Work wk = a.cluster ? small_work(a) : find_work<threads_of(GROUPS)>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
+  const Work wk = a.cluster ? small_work(a, blockIdx.x) : find_work<threads_of(GROUPS)>(a, reinterpret_cast<long long*>(smem + Layout::kOffScratch));
   if (blockIdx.x == 0 && wk.bad_len) atomicOr(sh.err(), LR_DEVERR_LEN);
   if (warp < kLoads) {
     attend<GROUPS>(a, sh, tmem);
@@ -589,7 +589,7 @@ kv8_attn_tc_kernel(const __grid_constant__ CUtensorMap mk, const __grid_constant
       const int bits = blockIdx.x == 0 ? check_all(a, lane, 32) : 0;
       if (bits) atomicOr(sh.err(), bits);
     } else if (lane == 0) {
-      write_pieces(a, wk);
+      reinterpret_cast<Pieces*>(a.split)[blockIdx.x] = pieces_of(a, wk, blockIdx.x);
     }
     __syncwarp();
     empty_rows<__nv_bfloat16>(a, blockIdx.x, gridDim.x);

@@ -1,5 +1,5 @@
-// Device helpers of the 8-bit paged cache: e4m3 conversions, and for the attention the division
-// of the batch's tiles among CTAs and the joining of the pieces of a split segment.
+// Device helpers of the 8-bit paged cache: e4m3 conversions, and for the attention what a CTA does to find its
+// share of the batch's tiles and to join the pieces of a split segment.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -8,6 +8,7 @@
 #include <math_constants.h>
 
 #include "lr_common.cuh"
+#include "kv8_rules.h"
 #include "lr_kv8.h"
 #include "sm100.cuh"
 
@@ -86,46 +87,7 @@ __device__ __forceinline__ float exp2_ftz(float x) {
   return y;
 }
 
-// ------------------------------------------------------------------ attention: the division of work
-//
-// A segment is one (sequence, KV head); its tokens are cut into tiles of two pages. The segments, in
-// the order of (sequence, head), are laid out on a line of units, one for each tile and kSegmentUnits at
-// the end for what a segment costs by itself, and the line is divided evenly among the CTAs: CTA c
-// takes units [c W / C, (c + 1) W / C), so ragged lengths cost nothing and one long sequence
-// fills the machine. A CTA's range touches at most two segments that others share: its first
-// and its last one. What it has of those are pieces (unnormalised sums with their maximum) in the
-// slots 2c and 2c + 1; a second kernel joins a segment's pieces in the order of the CTAs, which it finds
-// written down: CTA c does so for the segment that its range is the first to start inside of. (Joined by
-// the last CTA to finish instead, one of them was busy for 5 us with 8 pieces and 20 us with 37, its
-// own tiles waiting; with the division worked out again in the second kernel, that one took 6 us.)
-
-constexpr int kTilePages = 2;
-constexpr int kTileTokens = kTilePages * kBlock;
-constexpr int kSegmentUnits = 2;
-
-struct Span {
-  int lo, n;        // tokens [lo, n) are attended
-  int page0;        // page (index in the sequence) of the first tile
-  int tiles;        // tiles of one head
-  int units;        // its stretch of the line
-};
-
-__device__ __forceinline__ Span span_of(const Kv8AttnArgs& a, int len) {
-  Span s;
-  s.n = min(max(len, 0), a.max_pages * kBlock);
-  s.lo = a.window > 0 ? max(0, s.n - a.window) : 0;
-  s.page0 = s.lo / kBlock;
-  s.tiles = s.n == 0 ? 0 : ((s.n + kBlock - 1) / kBlock - s.page0 + kTilePages - 1) / kTilePages;
-  s.units = s.n == 0 ? 0 : s.tiles + kSegmentUnits;
-  return s;
-}
-__device__ __forceinline__ Span seq_span(const Kv8AttnArgs& a, int b) { return span_of(a, __ldg(a.lens + b)); }
-
-// First unit of CTA c's range.
-__device__ __forceinline__ long long range_begin(long long total, int c, int active) {
-  if (total <= INT_MAX / 2048) return (unsigned)total * (unsigned)c / (unsigned)active;  // active <= 1024: no 64-bit division
-  return total * c / active;
-}
+// ------------------------------------------------------------------ attention: the division of work (kv8_rules.h)
 
 // The lengths and the page table on their way to L2 while the grid before may still run: they are read one after the
 // other at the start, and after a step over many bytes they are in HBM again. Nothing is read
@@ -136,17 +98,6 @@ __device__ __forceinline__ void prefetch_inputs(const Kv8AttnArgs& a) {
   if (line * 32 < ids) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.table + line * 32));
   if (line * 32 < a.B) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.lens + line * 32));
 }
-
-// A CTA's range of units and where it starts.
-struct Work {
-  long long begin, end;
-  long long total;       // of the whole batch
-  int active;            // CTAs that have a range
-  int b;                 // sequence of the first unit
-  long long b_first;     // first unit of that sequence
-  bool bad_len;          // this thread has seen a length out of bounds
-  int pieces;            // small calls: CTAs of the cluster that have tiles
-};
 
 // Called by all NT threads of the CTA; `scratch` holds NT + 4 long longs of shared memory. Up to 32 sequences
 // are a warp's own business, a lane for each, without a barrier.
@@ -224,21 +175,6 @@ __device__ __forceinline__ Work find_work(const Kv8AttnArgs& a, long long* scrat
   return wk;
 }
 
-// Small calls: a cluster has a segment to itself, its CTAs the tiles in order, as many each as they take. The line
-// is that of the segment's sequence.
-__device__ __forceinline__ Work small_work(const Kv8AttnArgs& a) {
-  const int seg = blockIdx.x / a.cluster, rank = blockIdx.x % a.cluster;
-  Work wk{};
-  wk.b = seg / a.Hkv;
-  const Span sp = seq_span(a, wk.b);
-  if (sp.tiles == 0) return wk;
-  const int per = (sp.tiles + a.cluster - 1) / a.cluster, first = seg % a.Hkv * sp.units;
-  wk.pieces = (sp.tiles + per - 1) / per;
-  wk.begin = first + min(rank * per, sp.tiles);
-  wk.end = first + min((rank + 1) * per, sp.tiles);
-  return wk;
-}
-
 // Small calls: the device checks of every length and attended page, by the threads [0, step) of one CTA. They go through the
 // whole table (2048 ids at most), an id with its sequence's length: loads that depend on one another, sequence by
 // sequence, made this CTA 49 us late with 256 sequences.
@@ -255,63 +191,6 @@ __device__ __forceinline__ int check_all(const Kv8AttnArgs& a, int first, int st
   }
   return bits;
 }
-
-// The CTA whose range holds unit t, for total units over `active` CTAs: largest c with
-// c * total / active <= t.
-__device__ __forceinline__ int cta_of_unit(long long t, long long total, int active) {
-  if (total <= INT_MAX / 2048) return (int)(((unsigned)(t + 1) * (unsigned)active - 1) / (unsigned)total);
-  return (int)(((t + 1) * active - 1) / total);
-}
-
-// A place on the line that moves forward. It stays inside the batch even if somebody changes the lengths under the
-// kernel (a caller's mistake: then the result is garbage, and nothing else).
-struct Place {
-  int b, h;
-  Span sp;
-  long long b_first, seg_first;  // first unit of the sequence, of the segment
-  int tile;                      // >= sp.tiles in a segment's last units
-
-  __device__ __forceinline__ void start(const Kv8AttnArgs& a, const Work& wk) {
-    b = wk.b;
-    b_first = wk.b_first;
-    sp = seq_span(a, b);
-  }
-  __device__ __forceinline__ void seek(const Kv8AttnArgs& a, long long unit) {
-    while (unit >= b_first + (long long)sp.units * a.Hkv && b + 1 < a.B) {
-      b_first += (long long)sp.units * a.Hkv;
-      sp = seq_span(a, ++b);
-    }
-    const long long in = unit - b_first;
-    const int units = max(1, sp.units);
-    h = min(in <= INT_MAX ? (int)in / units : (int)min(in / units, (long long)INT_MAX), a.Hkv - 1);
-    seg_first = b_first + (long long)h * sp.units;
-    tile = (int)(unit - seg_first);
-  }
-};
-
-// Walks the segments of a CTA's range in order.
-struct Walk : Place {
-  const Kv8AttnArgs& a;
-  Work wk;
-  long long at;       // next unit
-  int tile0, tile1;   // the range's tiles of the current segment
-
-  __device__ Walk(const Kv8AttnArgs& a_, const Work& w) : a(a_), wk(w), at(w.begin) {
-    if (at < wk.end) start(a, wk);
-  }
-  // Moves to the next segment with tiles in the range; false at its end.
-  __device__ bool next() {
-    while (at < wk.end) {
-      seek(a, at);
-      at = max(at + 1, seg_first + sp.units);
-      tile0 = tile;
-      tile1 = (int)min((long long)sp.tiles, wk.end - seg_first);
-      if (tile0 < tile1) return true;
-    }
-    return false;
-  }
-  __device__ bool whole() const { return tile0 == 0 && tile1 == sp.tiles; }
-};
 
 // Sums of weights times values are kept in units of 2^32: a weight is 1 at most, so no number of tokens that an int
 // holds takes them out of fp32's range, whatever finite values the codes and scales stand for.
@@ -357,37 +236,6 @@ template <typename T>
 __device__ __forceinline__ T joined_value(const Kv8AttnArgs& a, size_t row, int d, const Joined& j, float acc) {
   const float prev = a.o_prev ? to_f32(((const T*)a.o_prev)[row * a.hd + d]) : 0.f;
   return from_f32<T>(join_value(acc, j.inv, prev, j.w_prev));
-}
-
-// ---- pieces of a split segment
-
-// The slot of this CTA's piece of a segment.
-__device__ __forceinline__ int piece_slot(const Work& wk, long long seg_first) {
-  return 2 * blockIdx.x + (wk.begin < seg_first ? 1 : 0);
-}
-
-// A split segment: b * Hkv + h, the CTAs that share it, and whether the first one's range starts before it (its
-// piece is its second one then).
-struct __align__(16) Pieces {
-  int head, n, c0, mid;
-  __device__ int slot(int i) const { return 2 * (c0 + i) + (i == 0 && mid ? 1 : 0); }
-};
-
-// Writes down the segment that this CTA's range is the first to start inside of, if any. One thread.
-__device__ __forceinline__ void write_pieces(const Kv8AttnArgs& a, const Work& wk) {
-  Pieces p{0, 0, 0, 0};
-  if (wk.begin < wk.end && blockIdx.x > 0) {
-    Place at;
-    at.start(a, wk);
-    at.seek(a, wk.begin);
-    if (at.tile > 0 && at.tile < at.sp.tiles && range_begin(wk.total, blockIdx.x - 1, wk.active) <= at.seg_first) {
-      p.head = at.b * a.Hkv + at.h;
-      p.c0 = cta_of_unit(at.seg_first, wk.total, wk.active);
-      p.n = cta_of_unit(at.seg_first + at.sp.tiles - 1, wk.total, wk.active) - p.c0 + 1;
-      p.mid = range_begin(wk.total, p.c0, wk.active) < at.seg_first;
-    }
-  }
-  reinterpret_cast<Pieces*>(a.split)[blockIdx.x] = p;
 }
 
 // o = 0 and lse = -inf, or the earlier partial result, for the sequences without tokens. One warp, `first` of `step`
