@@ -663,18 +663,7 @@ cudaError_t launch_append(const Kv8AppendArgs& a, int sm_count, cudaStream_t st)
   const int threads = kBlock * ((a.hd + 15) / 16);
   const int units = n_units(a);
   const int smem = ahead<T>() * 2 * 8 * (int)sizeof(T) * threads;
-  // Heads are shared out among up to 8 CTAs, which fill the machine evenly to the end. Each finds the page's angles
-  // again, though, so with more pages than SMs a share has eight query heads at least. Of 32 + 8 heads, 8
-  // shares and 4: 32K tokens 122 and 127 us by themselves, 132 and 133 in a long run; 24 ragged sequences 76
-  // and 74; 200 tokens each of 128 sequences 112 and 108. Of 8 + 8 heads, 8, 2 and one: 88, 70 and 68.
-  // Where most pages get a few tokens a share's beginning weighs more, and there are no more than run at once. 4
-  // tokens each of 64 sequences 12 us with 8, 9.4 with 4, 11 with 2; of 256 38 with 8, 24 with 2, 22 with one.
-  int ny = std::min(a.Hkv, 8);
-  if (a.n_tokens < (long long)kBlock / 2 * a.B) {
-    while (ny > 1 && (long long)units * ny > (long long)sm_count * (2048 / threads)) ny /= 2;
-  } else if (units > sm_count) {
-    ny = std::max(1, std::min(ny, a.Hq / 8));
-  }
+  const int ny = append_shares(a, threads, sm_count);
   void (*kernel)(Kv8AppendArgs, int) = kv8_append_kernel<T, Turn::kMixed>;
   if (a.hd % 16 == 0 && a.rot == 0) kernel = kv8_append_kernel<T, Turn::kNone>;
   else if (a.hd % 16 == 0 && a.rot == a.hd)

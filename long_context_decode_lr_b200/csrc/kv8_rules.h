@@ -53,6 +53,29 @@ LR_HD int sequence_of_unit(const Args& a, int u) {
   return b;
 }
 
+// CTAs that share a page's heads, each of `threads`. Up to 8 fill the machine evenly to the end, but each finds the
+// page's angles again. With more pages than SMs a share therefore has eight query heads at least. Of 32 + 8 heads of
+// 128 bf16 numbers, 8 shares and 4: 32K tokens 122 and 127 us by themselves, 132 and 133 in a long run; 24 ragged
+// sequences 76 and 74; 200 tokens each of 128 sequences 112 and 108. Of 8 + 8 heads, 8, 2 and one: 88, 70 and 68.
+// With under half a page of tokens for a sequence a share's beginning weighs more, and there are no more CTAs with
+// something to do than run at once and a third: 64 registers leave an SM 1024 threads, and a sequence touches one page
+// or two. The third was fitted; of 8, 4, 2 shares and one the best or within 4 % of it for 16 to 512 sequences of 2 to
+// 31 tokens and 2, 4, 6 or 8 KV heads, in bf16 with head_dim 64, 128 and 256 and in fp32 with 64 and 128; with 5
+// or 7 heads up to 1.3 times the best. 4 tokens each of 64 sequences 12.8, 9.9,
+// 11.6 and 17.7 us (it takes 4), 31 tokens 18.0, 15.6, 20.6 and 28.6 (4), fp32 32.7, 30.5, 50.9 and 56.4 (4), 4
+// tokens each of 256 sequences 40.6, 30.4, 25.6 and 23.1 (one).
+template <class Args>
+LR_HD int append_shares(const Args& a, int threads, int sm_count) {
+  int ny = least(a.Hkv, 8);
+  if (a.n_tokens < (long long)kPage / 2 * a.B) {
+    const long long pages = a.B + a.n_tokens / kPage, at_once = (long long)sm_count * (1024 / threads);
+    while (ny > 1 && 3 * pages * ny > 4 * at_once) ny = ny > 4 ? 4 : ny > 2 ? 2 : 1;
+  } else if (n_units(a) > sm_count) {
+    ny = most(1, least(ny, a.Hq / 8));
+  }
+  return ny;
+}
+
 // The positions [first, end) of a page of a sequence that receive new tokens.
 struct PageRows {
   int page;  // index in the sequence

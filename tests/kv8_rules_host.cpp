@@ -19,12 +19,15 @@ int kv8_page_rows(int p0, int n, int i, int* out) {
 }
 
 struct Append {
-  int B, n_tokens;
+  int B, n_tokens, Hkv, Hq;
   const int* cu;
 };
-int kv8_units(int B, int n_tokens) { return n_units(Append{B, n_tokens, nullptr}); }
-int kv8_unit_of(const int* cu, int B, int b) { return unit_of(Append{B, cu[B], cu}, b); }
-int kv8_sequence_of_unit(const int* cu, int B, int u) { return sequence_of_unit(Append{B, cu[B], cu}, u); }
+int kv8_units(int B, int n_tokens) { return n_units(Append{B, n_tokens, 1, 1, nullptr}); }
+int kv8_unit_of(const int* cu, int B, int b) { return unit_of(Append{B, cu[B], 1, 1, cu}, b); }
+int kv8_sequence_of_unit(const int* cu, int B, int u) { return sequence_of_unit(Append{B, cu[B], 1, 1, cu}, u); }
+int kv8_append_shares(int B, int n_tokens, int Hkv, int Hq, int threads, int sm_count) {
+  return append_shares(Append{B, n_tokens, Hkv, Hq, nullptr}, threads, sm_count);
+}
 
 // ---- attention
 

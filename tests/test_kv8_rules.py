@@ -68,6 +68,27 @@ def test_append_units(rules):
                 taken.add(u)
 
 
+def test_append_shares(rules):
+    """At least one share of a page's heads and at most one for each KV head; with few tokens per sequence no more
+    CTAs with something to do than a third over what is resident. The shapes named beside the rule."""
+    rng = random.Random(8)
+    for _ in range(2000):
+        B, hkv, group = rng.randint(1, 600), rng.randint(1, 40), rng.randint(1, 8)
+        hd = 8 * rng.randint(1, 32)
+        threads = 64 * -(-hd // 16)
+        n = B * rng.randint(0, 31) + rng.randint(0, B - 1)
+        ny = rules.kv8_append_shares(B, n, hkv, hkv * group, threads, 148)
+        assert 1 <= ny <= min(hkv, 8)
+        if n < 32 * B:
+            assert ny == 1 or (B + n // 64) * ny * 3 <= 148 * (1024 // threads) * 4
+    for B, new, hkv, hq, hd, want in ((64, 4, 8, 32, 128, 4), (64, 31, 8, 32, 128, 4), (256, 4, 8, 32, 128, 1), (64, 31, 8, 32, 64, 8),
+                                      (64, 31, 4, 16, 256, 2), (64, 4, 6, 48, 128, 4), (128, 10, 6, 48, 128, 2), (1, 20, 8, 32, 128, 8),
+                                      (1, 32768, 8, 32, 128, 4), (128, 200, 8, 32, 128, 4), (128, 200, 8, 8, 128, 1)):
+        assert rules.kv8_append_shares(B, B * new, hkv, hq, 64 * -(-hd // 16), 148) == want, (B, new, hkv, hq, hd)
+    assert rules.kv8_append_shares(1 << 20, (1 << 31) - 1, 8, 32, 512, 148) == 4  # nothing wraps
+    assert rules.kv8_append_shares(1 << 26, 1 << 30, 8, 32, 512, 148) == 1
+
+
 def _divide(rules, lens, hkv, max_pages, window, n_cta, cluster, visit=-1):
     """(pieces of every segment, written-down segments) as the CTAs find them."""
     arr = (ctypes.c_int * len(lens))(*lens)
