@@ -439,7 +439,7 @@ lr_status lr_decode_attn_lse(const lr_cache_shape* shape, int32_t layer, int32_t
  * dtype is the type of q, k, v and o beside the cache. A scale covers one page of one KV head.
  */
 typedef struct lr_kv8_pages {
-  int32_t batch;      /* B >= 0 */
+  int32_t batch;      /* B >= 0, at most 2^26; B times the heads of q, k and v under 2^31 */
   int32_t n_kv_heads; /* Hkv >= 1 */
   int32_t head_dim;   /* hd: multiple of 8, <= 256 */
   int32_t n_pages;    /* pages in the pool, >= 1 */

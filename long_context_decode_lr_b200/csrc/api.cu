@@ -86,6 +86,7 @@ lr_status check_kv8(const lr_kv8_pages* kv) {
   if (kv->head_dim % 8 || kv->head_dim > 256) return fail(LR_ERR_UNSUPPORTED, "head_dim must be a multiple of 8 and <= 256");
   if (kv->n_kv_heads > (1 << 20) / kv->head_dim) return fail(LR_ERR_UNSUPPORTED, "key width too large");
   if (kv->max_pages > INT32_MAX / LR_BLOCK_TOKENS) return fail(LR_ERR_UNSUPPORTED, "max_pages too large");
+  if (kv->batch > 1 << 26) return fail(LR_ERR_UNSUPPORTED, "batch too large");
   const int64_t dense = (int64_t)kv->n_kv_heads * LR_BLOCK_TOKENS * kv->head_dim;
   if (kv->page_stride && (kv->page_stride < dense || kv->page_stride % 16))
     return fail(LR_ERR_INVALID_ARG, "page_stride must be 0 or a multiple of 16 of at least one page's bytes");
@@ -102,6 +103,7 @@ lr_status check_kv8_heads(const lr_kv8_pages* kv, int32_t n_q_heads) {
   if (n_q_heads < 1 || n_q_heads % kv->n_kv_heads)
     return fail(LR_ERR_INVALID_ARG, "n_q_heads must be a positive multiple of n_kv_heads");
   if (n_q_heads / kv->n_kv_heads > 8) return fail(LR_ERR_UNSUPPORTED, "more than 8 query heads per KV head");
+  if ((int64_t)kv->batch * n_q_heads > INT32_MAX) return fail(LR_ERR_UNSUPPORTED, "batch * n_q_heads too large");
   return LR_OK;
 }
 
@@ -511,6 +513,8 @@ lr_status lr_kv8_append(const lr_kv8_pages* kv, int32_t n_q_heads, int32_t n_tok
   if ((q != nullptr) != (q_out != nullptr)) return fail(LR_ERR_INVALID_ARG, "q and q_out go together");
   if (q && (n_q_heads < 1 || n_q_heads > (1 << 20) / kv->head_dim))
     return fail(LR_ERR_INVALID_ARG, "n_q_heads=%d out of range", n_q_heads);
+  if ((int64_t)kv->batch * (kv->n_kv_heads + (q ? n_q_heads : 0)) > INT32_MAX)
+    return fail(LR_ERR_UNSUPPORTED, "batch * heads too large");
   int rot = 0;
   if (rope) {
     rot = rope->rot_dim;

@@ -184,3 +184,23 @@ def test_small_calls(rules):
             _check(rules, lens, hkv, width, rng.choice([0, 0, 100]), B * hkv * c, cluster=c, visit=16)
     assert clusters == {1, 2, 4, 8}
     assert [rules.kv8_small_cluster(0, 8, 1, 1), rules.kv8_small_cluster(1 << 30, 1 << 10, 1, 1)] == [0, 0]
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from long_context_decode_lr_b200 import lowram as lr
+    lrbuild.build()
+    return lr.library()
+
+
+@pytest.mark.parametrize("batch,hkv,hq", [((1 << 26) + 1, 1, 1), (1 << 26, 8, 32), (1 << 20, 2048, 2048), (1 << 14, 1 << 17, 1 << 17)])
+def test_sizes_past_an_int_are_refused(lib, batch, hkv, hq):
+    """Batches whose units, warps or heads an int does not count."""
+    from long_context_decode_lr_b200 import lowram as lr
+    P = 0x10000
+    kv = ctypes.byref(lr.lr_kv8_pages(batch, hkv, 8, 10, 4, lr.LR_BF16, 0, P, P, P, P, P, P))
+    assert lib.lr_kv8_append(kv, hq, batch, None, None, P, 0, P, 0, P, 0, P, P, 256, None) == lr.LR_ERR_UNSUPPORTED
+    assert lib.lr_decode_attn_kv8(kv, hq, P, 0, 0.0, None, None, P, None, P, 1 << 50, None) == lr.LR_ERR_UNSUPPORTED
+    assert lib.lr_kv8_attn_workspace_bytes(kv, hq) == 0
+    if batch <= 1 << 26 and batch * hkv < 1 << 31:  # without queries an append of it is fine as far as the host goes
+        assert lib.lr_kv8_append(kv, 0, batch, None, None, None, 0, P, 0, P, 0, None, P, 255, None) == lr.LR_ERR_WORKSPACE
