@@ -421,7 +421,7 @@ def lr_decode_attn_kv8(kv: Kv8Pages, n_q_heads, q, o, ws, lse=None, window=0, sc
     """One decode step over the 8-bit paged cache: q, o [B, Hq, hd]; lse [B, Hq] fp32 (optional);
     o_prev, lse_prev: an earlier partial result over other tokens, joined to the same softmax."""
     b, shape = kv.batch, (kv.batch, n_q_heads)
-    args = (kv.ref, n_q_heads, kv._dense_rows(q, b, n_q_heads, "q"), int(window), float(scale),
+    args = (kv.ref, n_q_heads, kv._dense_rows(q, b, n_q_heads, "q"), min(int(window), 0x7fffffff), float(scale),
             None if o_prev is None else kv._dense_rows(o_prev, b, n_q_heads, "o_prev"),
             None if lse_prev is None else kv._beside(lse_prev, torch.float32, shape, "lse_prev"),
             kv._dense_rows(o, b, n_q_heads, "o"), None if lse is None else kv._beside(lse, torch.float32, shape, "lse"))

@@ -156,3 +156,15 @@ def test_rotation_angles_at_every_position(single, pos, dtype):
     angles = np.array([float(a - TWO_PI * (a // TWO_PI)) for a in angles])
     want = np.concatenate([np.cos(angles), np.sin(angles)])
     assert (np.abs(got - want) <= (2.0 ** -20 if dtype == "bf16" else 2.0 ** -22) + HALF[dtype] * np.abs(want)).all()
+
+
+def test_window_past_an_int_is_the_whole_sequence():
+    rng = np.random.default_rng(2)
+    pool = Pool(rng, [200], 1, 128)
+    q, _ = rounded(rng.standard_normal((1, 4, 128)), "bf16")
+    o, lse, _ = attend(pool, q)
+    for window in (2 ** 31, 2 ** 32 + 64, 10 ** 12):
+        o2, lse2, err = attend(pool, q, window=window)
+        assert err == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
+    with pytest.raises(RuntimeError):
+        attend(pool, q, window=-1)
