@@ -66,7 +66,8 @@ __device__ __forceinline__ uint32_t codes2(float lo, float hi, float inv) {
   return e4m3x2(or_nan(lo) * inv, or_nan(hi) * inv);
 }
 // A page may hold a scale of the caller's that is no power of two, and then its fp32 reciprocal is a rounded one:
-// numbers are divided. (Where no page does, that costs a call of one token under 0.1 us and a mixed one 2 of 71 us.)
+// numbers are divided. (Where no page does, that costs a call of one token under 0.1 us, 24 ragged sequences 2 of
+// 71 us and 32K tokens nothing; with the division out of line 4 and 2 us, a product of fp64 numbers instead 3 and 2.)
 __device__ __forceinline__ bool is_pow2(float s) { return (__float_as_uint(s) & 0x7fffffu) == 0; }
 
 // Four codes scaled again by `ratio`.
@@ -318,13 +319,6 @@ __device__ __forceinline__ uint2 codes8(const float (&v)[8], float inv) {  // nu
   u.x = e4m3x2(x[0], x[1]) | (e4m3x2(x[2], x[3]) << 16);
   u.y = e4m3x2(x[4], x[5]) | (e4m3x2(x[6], x[7]) << 16);
   return u;
-}
-
-__device__ __forceinline__ uint2 divided_codes8(const float (&v)[8], float s) {
-  float x[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) x[i] = __fdiv_rn(v[i], s);
-  return codes8(x, 1.f);
 }
 
 // Sines, negative sines and cosines of a thread's 8 angles.
@@ -619,7 +613,8 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
     }
     if (tid < 2) *(tid ? scale[1] : scale[0]) = tid ? now[1] : now[0];
     if (in) {
-      const float ik = __frcp_rn(now[0]), iv = __frcp_rn(now[1]);
+      const bool dk = !is_pow2(now[0]), dv = !is_pow2(now[1]);
+      const float ik = dk ? 1.f : __frcp_rn(now[0]), iv = dv ? 1.f : __frcp_rn(now[1]);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         if (x && !two) break;
@@ -633,8 +628,16 @@ __global__ void __launch_bounds__(1024) kv8_append_kernel(Kv8AppendArgs a, int n
             kx[x][i] = or_nan(kx[x][i]);
           }
         }
-        *reinterpret_cast<uint2*>(head[0] + row + at) = is_pow2(now[0]) ? codes8(kx[x], ik) : divided_codes8(kx[x], now[0]);
-        *reinterpret_cast<uint2*>(head[1] + row + at) = is_pow2(now[1]) ? codes8(v, iv) : divided_codes8(v, now[1]);
+        if (dk) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) kx[x][i] = __fdiv_rn(kx[x][i], now[0]);
+        }
+        if (dv) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) v[i] = __fdiv_rn(v[i], now[1]);
+        }
+        *reinterpret_cast<uint2*>(head[0] + row + at) = codes8(kx[x], ik);
+        *reinterpret_cast<uint2*>(head[1] + row + at) = codes8(v, iv);
       }
     }
     if (in) {
