@@ -74,3 +74,21 @@ def attention(q, K, V, scale, split_q=lambda x: x, split_p=lambda x: x):
     p = np.exp(s - s.max(1, keepdims=True))
     total = p.sum(1, keepdims=True)
     return split_p(p) @ V / total, s.max(1) + np.log(total[:, 0]), p @ np.abs(V) / total
+
+
+def per_token_limit(q, K, V, scale, bf16, prev=None):
+    """(o, lse, limit of o, limit of lse) of one head in fp64. A score is a sum of fp32 products, off by at most
+    (hd + 12) u scale sum |q||k| of its own token; its weight by that, the exponential and the split relative to
+    its own size, and all of them by the sum's relative error. prev: (o_prev, lse_prev), exact."""
+    s, slack, vals = scale * K @ q, (K.shape[1] + 12) * U * scale * np.abs(K) @ np.abs(q), V
+    if prev is not None:
+        s, slack, vals = np.append(s, prev[1]), np.append(slack, 2 * U * abs(prev[1])), np.concatenate([V, prev[0][None]])
+    p = np.exp(s - s.max())
+    w = p / p.sum()
+    # an fp32 score in units of log 2, and the largest one that it is taken from
+    own = np.expm1(slack + 4 * U * (np.abs(s) + np.abs(s).max())) + (2.0 ** -11 if bf16 else 2.0 ** -21) + len(s) * U
+    weight = w * (own + (w * own).sum())
+    o = w @ vals
+    half = 2.0 ** -8 if bf16 else 2.0 ** -24
+    lse = s.max() + np.log(p.sum())
+    return o, lse, weight @ np.abs(vals) + half * np.abs(o) + 2.0 ** -27 * np.abs(vals).max(0), (w * own).sum() + 8 * U * abs(lse)

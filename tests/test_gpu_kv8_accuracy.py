@@ -97,3 +97,26 @@ def test_fp32_norm(lens, hd, G, width):
     ref, rl, mass = orc.decode(qr, pool.kc, pool.vc, pool.ks, pool.vs, pool.table, pool.lens, hd ** -0.5)
     assert err == 0
     assert np.linalg.norm(o.double().cpu().numpy() - ref) <= acc.L2_LIMIT * np.linalg.norm(mass)
+
+
+@pytest.mark.parametrize("spread", [3.0, 300.0])
+@pytest.mark.parametrize("hd,dtype", [(128, "bf16"), (64, "f32"), (128, "f32"), (256, "bf16")])
+def test_every_number_within_its_own_tokens_limit(hd, dtype, spread):
+    """Scores of a few and of hundreds, alone and joined with an earlier part near, under and over them."""
+    rng = np.random.default_rng(hd + int(spread))
+    pool = Pool(rng, [500], 2, hd, dtype)
+    q, qr = rounded(rng.standard_normal((1, 8, hd)) * spread, dtype)
+    scale, t = hd ** -0.5, np.arange(500)
+    pages = pool.table[0, t // 64]
+    for lp in (None, -1e4, 3.0 * spread, 1e4):
+        prev, prev_ref = None, None
+        if lp is not None:
+            po, por = rounded(rng.standard_normal((1, 8, hd)), dtype)
+            prev, prev_ref = (po, torch.full((1, 8), lp, device="cuda")), (por, lp)
+        o, lse, err = attend(pool, q, prev=prev)
+        assert err == 0
+        for g in range(8):
+            K, V = (orc.E4M3[c[pages, g // 4, t % 64]] * s[pages, g // 4][:, None].astype(np.float64) for c, s in ((pool.kc, pool.ks), (pool.vc, pool.vs)))
+            ro, rl, lim, llim = acc.per_token_limit(qr[0, g], K, V, scale, dtype == "bf16", None if prev is None else (prev_ref[0][0, g], lp))
+            assert (np.abs(o[0, g].double().cpu().numpy() - ro) <= lim).all()
+            assert abs(float(lse[0, g]) - rl) <= llim
