@@ -480,7 +480,7 @@ size_t lr_kv8_append_workspace_bytes(const lr_kv8_pages* kv);
  * tokens, with a = the largest finite magnitude among this call's rows of it:
  *   fresh = the smallest power of two with a <= 448 fresh, at least 2^-24;
  *   scale = max(scale, fresh) where the page already holds tokens of the sequence: if that is
- *           larger than the old scale, their codes become round(code * old / scale);
+ *           larger than the old scale, their codes become round(code * (old / scale)), one fp32 product;
  *   scale = fresh where it does not (what the page and its scale held before is not read);
  *   code  = round(x / scale), to nearest even, x / scale one fp32 division (exact where the scale is a
  *           power of two); NaN and infinities become NaN codes and do not count towards a.

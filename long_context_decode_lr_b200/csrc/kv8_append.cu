@@ -12,8 +12,8 @@
 // whole turns by itself and stays right to 2^-32 of a turn at far positions; sine and cosine take the top 32 bits.
 //
 // Measured (B200, 32 query and 8 KV heads of 128 bf16 numbers, all rotated): 32K tokens of one sequence
-// 127 us (133 in a long run), 5.8 TB/s of the 738 MB read and written; one token for each of 64 sequences 3.4 us.
-// fp32 335 us, 4.2 TB/s, rotated or not: its warps wait for the memory queue, with the issue slots and HBM half idle.
+// 127 us (132 in a long run), 5.8 TB/s of the 738 MB read and written; one token for each of 64 sequences 3.4 us.
+// fp32 321 to 335 us, 4.2 to 4.4 TB/s, rotated or not: its warps wait for the memory queue, with the issue slots and HBM half idle.
 // Lanes that exchange their 16-byte parts, so that an instruction covers whole sectors or lines, took 354 and 362.
 #include <algorithm>
 
