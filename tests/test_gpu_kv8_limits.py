@@ -168,3 +168,58 @@ def test_window_past_an_int_is_the_whole_sequence():
         assert err == 0 and torch.equal(o, o2) and torch.equal(lse, lse2)
     with pytest.raises(RuntimeError):
         attend(pool, q, window=-1)
+
+
+@pytest.mark.parametrize("width", [None, 600], ids=["", "room_for_more"])
+@pytest.mark.parametrize("hd,dtype", [(128, "bf16"), (64, "f32")])
+@pytest.mark.parametrize("before", ["nothing", "memcpy", "memset", "two_streams", "itself"])
+def test_attention_captured_behind(before, hd, dtype, width):
+    """A captured call that starts the graph, or follows a copy of its lengths, a memset, work joined from another
+    stream or another call whose result it takes; replayed with other inputs, equal to the same calls without a graph."""
+    rng = np.random.default_rng(hd)
+    pool = Pool(rng, [300, 200], 2, hd, dtype, width=width)
+    src, lens = pool.dev[5].clone(), pool.dev[5]
+    q, _ = rounded(rng.standard_normal((2, 8, hd)), dtype)
+    prev_o, prev_lse, scratch = torch.randn_like(q), torch.randn((2, 8), device="cuda"), torch.empty(64, device="cuda")
+    first = (torch.empty_like(q), torch.empty((2, 8), device="cuda"))
+    out = (torch.empty_like(q), torch.empty((2, 8), device="cuda"))
+    need = lr.lr_kv8_attn_workspace_bytes(pool.kv, 8)
+    ws, ws2, side = lr.workspace(need), lr.workspace(need), torch.cuda.Stream()
+
+    def call():
+        if before == "memcpy":
+            lens.copy_(src)
+        elif before == "memset":
+            scratch.zero_()
+        elif before == "two_streams":
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                lens.copy_(src)
+            scratch.zero_()
+            torch.cuda.current_stream().wait_stream(side)
+        elif before == "itself":
+            lr.lr_decode_attn_kv8(pool.kv, 8, q, first[0], ws2, lse=first[1], window=100)
+        p = first if before == "itself" else (prev_o, prev_lse)
+        lr.lr_decode_attn_kv8(pool.kv, 8, q, out[0], ws, lse=out[1], o_prev=p[0], lse_prev=p[1])
+
+    st = torch.cuda.Stream()
+    st.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(st):
+        call()
+    torch.cuda.current_stream().wait_stream(st)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for n in ([300, 200], [0, 17], [129, 300]):
+        host = torch.tensor([min(n[0], 300), min(n[1], 200)], dtype=torch.int32)
+        src.copy_(host)
+        if before not in ("memcpy", "two_streams"):
+            lens.copy_(src)
+        q.copy_(torch.randn_like(q))
+        out[0].fill_(7.0), out[1].fill_(7.0)
+        graph.replay()
+        got = [t.clone() for t in out]
+        out[0].fill_(5.0), out[1].fill_(5.0)
+        call()
+        assert lr.lr_get_device_error(ws) == 0
+        assert torch.equal(got[0], out[0]) and torch.equal(got[1], out[1]) and torch.isfinite(out[0].float()).all()
