@@ -467,7 +467,7 @@ __device__ void attend(const Kv8AttnArgs& a, const Shared& sh, uint32_t tmem) {
       }
       reinterpret_cast<uint4*>(sh.weights(it & 1))[group * kTileTokens + tid] =
           make_uint4(term[0][0] | (term[0][1] << 16), term[1][0] | (term[1][1] << 16), term[2][0] | (term[2][1] << 16), 0u);
-      if (meta.t0 < meta.lo || meta.t0 + kTileTokens > meta.n || !both) {
+      if (meta.t0 < meta.lo || meta.n - meta.t0 < kTileTokens || !both) {
         // value rows outside the attended tokens may hold anything, NaN codes among it
         wait(V_FULL + s, ph);
         if (!seen && group == 0) {

@@ -223,3 +223,23 @@ def test_attention_captured_behind(before, hd, dtype, width):
         call()
         assert lr.lr_get_device_error(ws) == 0
         assert torch.equal(got[0], out[0]) and torch.equal(got[1], out[1]) and torch.isfinite(out[0].float()).all()
+
+
+@pytest.mark.parametrize("window", [1, 63, 64, 65, 130, 200])
+@pytest.mark.parametrize("behind", [0, 1, 64, 77])
+@pytest.mark.parametrize("hd,dtype", [(128, "bf16"), (64, "f32")])
+def test_attention_at_the_end_of_the_longest_table(hd, dtype, behind, window):
+    """The last tokens of a sequence of 64 (2^25 - 1) tokens, or a few less: the same as of a short one."""
+    rng = np.random.default_rng(window + behind)
+    width = (1 << 25) - 1
+    short = Pool(rng, [64 * 5 - behind], 1, hd, dtype, room=[64 * 5])
+    table = torch.full((1, width), -1, dtype=torch.int32, device="cuda")
+    table[0, width - 5:] = short.dev[4][0, :5]
+    lens = torch.tensor([64 * width - behind], dtype=torch.int32, device="cuda")
+    kv = lr.Kv8Pages(*short.dev[:4], table, lens, DT[dtype])
+    q, qr = rounded(rng.standard_normal((1, 4, hd)), dtype)
+    o, lse, ws = torch.empty_like(q), torch.empty((1, 4), device="cuda"), lr.workspace(lr.lr_kv8_attn_workspace_bytes(kv, 4))
+    lr.lr_decode_attn_kv8(kv, 4, q, o, ws, lse=lse, window=window)
+    assert lr.lr_get_device_error(ws) == 0
+    ref = orc.decode(qr, short.kc, short.vc, short.ks, short.vs, short.table, short.lens, hd ** -0.5, window)
+    check_attention((o, lse), ref, short, qr, hd ** -0.5, 200)
